@@ -360,3 +360,8 @@ def e4m3_encode(v: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Te
         out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
     _abi.call("fp4q_e4m3_encode", v.data_ptr(), v.numel(), out.data_ptr(), _stream())
     return out
+
+
+from .experts import (ACTIVATIONS, ExpertPlan, ExpertWeights, expert_combine,  # noqa: E402,F401
+                      expert_combine_bwd, expert_gemm, expert_quantize, expert_rows, expert_sort,
+                      expert_weights, glu_bwd, glu_quantize)

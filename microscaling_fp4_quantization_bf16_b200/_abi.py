@@ -1,4 +1,5 @@
-"""ctypes declarations of the C ABI in include/fp4q.h (libfp4q.so).
+"""ctypes declarations of the C ABI in include/fp4q.h and fp4q_experts.h
+(libfp4q.so).
 
 Argument marshalling only: every step of quantization runs in the CUDA
 kernels behind these entry points. Loading fails loudly when the library has
@@ -46,6 +47,23 @@ SIGNATURES = {
     "fp4q_device_errors": (_i32, []),
 }
 
+# Every symbol declared in include/fp4q_experts.h.
+EXPERT_SIGNATURES = {
+    "fp4q_expert_rows": (_i64, [_i64, _i64]),
+    "fp4q_expert_sort_work": (_i64, [_i64, _i64]),
+    "fp4q_expert_sort": (_i32, [_p, _i32, _i64, _i64, _p, _p, _p, _p, _p]),
+    "fp4q_expert_quantize": (_i32, [_p, _i64, _i64, _i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p,
+                                    _p, _p, _p, _i32, _p]),
+    "fp4q_expert_gemm": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32,
+                                _i64, _p, _i32, _p]),
+    "fp4q_glu_quantize": (_i32, [_p, _i64, _i64, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _p,
+                                 _p, _p, _p, _i32, _p]),
+    "fp4q_glu_bwd": (_i32, [_p, _p, _i64, _i64, _p, _i64, _i32, _i32, _p, _p]),
+    "fp4q_expert_combine": (_i32, [_p, _i32, _i64, _i64, _p, _i64, _i32, _p, _i32, _p, _i32, _p]),
+    "fp4q_expert_combine_bwd": (_i32, [_p, _i32, _p, _i32, _i64, _i64, _p, _i64, _i32, _p, _p, _p,
+                                       _p]),
+}
+
 _lib = None
 _lock = threading.Lock()
 
@@ -66,7 +84,7 @@ def load(path: str = LIB_PATH):
                     f"CUDA library {path} is missing: run "
                     "`python -m microscaling_fp4_quantization_bf16_b200.build` (needs nvcc)")
             lib = C.CDLL(path)
-            for name, (res, args) in SIGNATURES.items():
+            for name, (res, args) in {**SIGNATURES, **EXPERT_SIGNATURES}.items():
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args

@@ -13,6 +13,7 @@
 
 #include "fp4q.h"
 
+#include "experts.h"
 #include "internal.h"
 
 using namespace fp4q;
@@ -282,6 +283,25 @@ fp4q_status gemm_args_status(const uint8_t* a_codes, const uint8_t* a_mma_scales
 cudaError_t injected_launch_error() { return injected(); }
 
 fp4q_status record_cuda_error(cudaError_t e) { return cuda_status(e); }
+
+cudaError_t device_error_word(unsigned** p)
+{
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp4q_device_errors);
+}
+
+bool make_byte_map(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_rows)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr)
+        return false;
+    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace fp4q
 

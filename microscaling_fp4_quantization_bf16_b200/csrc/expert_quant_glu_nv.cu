@@ -1,0 +1,53 @@
+// expert_quant_glu_nv.cu -- gated activation quantized to NVFP4, and its abs-max.
+#include "expert_quant.cuh"
+
+namespace fp4q {
+
+namespace {
+
+template <int ROT>
+__global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, int64_t ntiles)
+{
+    pdl_begin();
+    const int lane = threadIdx.x & 31;
+    unsigned m = 0;
+    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
+    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += (int64_t)gridDim.x * QTHREADS) {
+        if (s - lane >= a.nseg)  // warp-uniform
+            break;
+        const uint32_t i = (uint32_t)s / a.spr;
+        float y[SEG];
+        load_glu(a, s < a.nseg ? row_of(a, i, 0) : -1, (uint32_t)s - i * a.spr, y);
+        rotate_seg<ROT>(y, lane);
+#pragma unroll
+        for (int k = 0; k < SEG; ++k)
+            m = max(m, __float_as_uint(fabsf(y[k])));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0 && m != 0)
+        atomicMax(a.amax_out, m);  // a maximum does not depend on the order
+}
+
+}  // namespace
+
+cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, cudaStream_t st)
+{
+    switch (rot) {
+    case 0: return launch_rows(glu_amax_kernel<0>, a, st);
+    case 16: return launch_rows(glu_amax_kernel<16>, a, st);
+    case 32: return launch_rows(glu_amax_kernel<32>, a, st);
+    case 64: return launch_rows(glu_amax_kernel<64>, a, st);
+    case 128: return launch_rows(glu_amax_kernel<128>, a, st);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_glu_quant_nv(int strat, int rot, const RowQuantArgs& a, cudaStream_t st)
+{
+    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_ABSMAX)
+    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_PREVENT_ZERO)
+    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_FOUR_OVER_SIX)
+    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_BRUTE_FORCE)
+    return cudaErrorInvalidValue;
+}
+}  // namespace fp4q

@@ -1,0 +1,363 @@
+"""One mixture-of-experts feed-forward layer in FP4: the torch side of
+include/fp4q_experts.h.
+
+    plan = expert_sort(ids, experts)                        # rows of the expert order
+    qa = expert_quantize(x, plan, "nvfp4")                  # tokens -> quantized rows
+    gu = expert_gemm(qa.codes, qa.scales, qa.global_scale, up.codes, up.scales,
+                     up.global_scale, plan, "nvfp4")        # gate and value of every row
+    qh = glu_quantize(gu, "nvfp4", plan=plan)               # silu(gate) * value, quantized
+    y = expert_gemm(qh.codes, qh.scales, qh.global_scale, down.codes, down.scales,
+                    down.global_scale, plan, "nvfp4")
+    out = expert_combine(y, plan, weights)                  # weighted sum back to tokens
+
+The weights are laid out once by expert_weights(). Every function runs on the
+current stream of its tensors' device and allocates its outputs with torch
+(unless given preallocated ones); nothing reads a size back from the device,
+so a whole layer can be captured in a CUDA graph. Rows of the padded layout
+that hold no choice are left as they were.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional, Tuple
+
+import torch
+
+from . import _abi
+
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+SEGMENT_ROWS = 128
+_FORMATS = {"nvfp4": 0, "mxfp4": 1}
+_STRATEGIES = {"absmax": 0, "prevent_zero": 1, "four_over_six": 2, "brute_force": 3}
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+@dataclass
+class ExpertPlan:
+    """Where each choice's row is (see include/fp4q_experts.h)."""
+    counts: torch.Tensor   # int32 [experts]: choices of each expert
+    starts: torch.Tensor   # int32 [experts + 1]: first row of each, a multiple of 128
+    slots: torch.Tensor    # int32 [tokens, k]: row of each choice, -1 if dropped
+    rows: int              # rows of the padded layout, a multiple of 128
+
+
+@dataclass
+class ExpertWeights:
+    """One weight matrix per expert in the product's operand form."""
+    codes: torch.Tensor                   # uint8 [experts, N, K/2]
+    scales: torch.Tensor                  # uint8 [experts, mma_scale_bytes(N, K)]
+    global_scale: Optional[torch.Tensor]  # float32 [experts] (NVFP4) or None
+
+
+def _need(t, name: str, dtype, *shape) -> None:
+    """t is a contiguous CUDA tensor of dtype (or one of several) and shape (None: any)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape and (t.dim() != len(shape) or any(s is not None and s != d
+                                               for s, d in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _fmt(fmt) -> int:
+    f = _FORMATS.get(fmt) if isinstance(fmt, str) else fmt
+    if f not in (0, 1):
+        raise ValueError(f"fmt must be 'nvfp4' or 'mxfp4', got {fmt!r}")
+    return f
+
+
+def _strategy(s) -> int:
+    v = _STRATEGIES.get(s) if isinstance(s, str) else s
+    if v not in (0, 1, 2, 3):
+        raise ValueError(f"unknown strategy {s!r}")
+    return v
+
+
+def _act(act) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """Calls an entry point on the current stream of `device`."""
+    if device.index == torch.cuda.current_device():
+        _abi.call(name, *args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            _abi.call(name, *args, torch.cuda.current_stream().cuda_stream)
+
+
+def _same_device(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _plan_args(plan: ExpertPlan, device) -> None:
+    _need(plan.slots, "plan.slots", torch.int32, None, None)
+    _same_device(device, plan.slots)
+    if plan.rows < 0 or plan.rows % SEGMENT_ROWS:
+        raise ValueError(f"plan.rows must be a multiple of {SEGMENT_ROWS}, got {plan.rows}")
+
+
+def scale_bytes(rows: int, cols: int, fmt="nvfp4") -> int:
+    """Bytes of the MMA-layout scales of [rows, cols] (0 rows or columns: 0)."""
+    blocks = cols // (16 if _fmt(fmt) == 0 else 32)
+    return -(-rows // 128) * 128 * (-(-blocks // 4) * 4)
+
+
+def expert_rows(choices: int, experts: int) -> int:
+    """Rows of the padded layout that hold any routing of `choices` choices."""
+    rows = _abi.load().fp4q_expert_rows(choices, experts)
+    if rows < 0:
+        raise ValueError(f"no row layout for {choices} choices among {experts} experts")
+    return rows
+
+
+def expert_sort(ids: torch.Tensor, experts: int, rows: Optional[int] = None,
+                out: Optional[ExpertPlan] = None) -> ExpertPlan:
+    """Sorts the router's choices ids (int32 or int64 [tokens, k]) by expert,
+    stably. An id outside 0 .. experts-1 drops the choice. rows: rows of the
+    layout, at least the default expert_rows(tokens * k, experts)."""
+    _need(ids, "ids", (torch.int32, torch.int64), None, None)
+    lib = _abi.load()
+    n = ids.numel()
+    least = expert_rows(n, experts)
+    if out is None:
+        out = ExpertPlan(ids.new_empty(experts, dtype=torch.int32),
+                         ids.new_empty(experts + 1, dtype=torch.int32),
+                         ids.new_empty(ids.shape, dtype=torch.int32), least if rows is None else rows)
+    else:
+        _need(out.counts, "out.counts", torch.int32, experts)
+        _need(out.starts, "out.starts", torch.int32, experts + 1)
+        _need(out.slots, "out.slots", torch.int32, *ids.shape)
+        _same_device(ids.device, out.counts, out.starts, out.slots)
+    if out.rows < least or out.rows % SEGMENT_ROWS:
+        raise ValueError(f"rows must be a multiple of {SEGMENT_ROWS} and at least {least}, got {out.rows}")
+    size = lib.fp4q_expert_sort_work(n, experts)
+    work = ids.new_empty(size // 4, dtype=torch.int32) if size else None
+    _call("fp4q_expert_sort", ids.device, ids.data_ptr(), ids.element_size(), n, experts,
+          out.counts.data_ptr(), out.starts.data_ptr(), out.slots.data_ptr(), _ptr(work))
+    return out
+
+
+def _quantized_out(out, rows: int, cols: int, f: int, dq_dtype, device):
+    """The given Quantized, checked, or a new one for [rows, cols] in the MMA layout."""
+    from . import Quantized
+    size = scale_bytes(rows, cols, f)
+    if out is None:
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+        return Quantized(new((rows, cols // 2), torch.uint8), new((size,), torch.uint8),
+                         new((1,), torch.float32) if f == 0 else None, None,
+                         new((rows, cols), dq_dtype) if dq_dtype is not None else None)
+    _need(out.codes, "out.codes", torch.uint8, rows, cols // 2)
+    _need(out.scales, "out.scales", torch.uint8, size)
+    if f == 0:
+        _need(out.global_scale, "out.global_scale", torch.float32, 1)
+    if out.dq is not None:
+        _need(out.dq, "out.dq", (torch.float32, torch.bfloat16), rows, cols)
+    _same_device(device, out.codes, out.scales, out.global_scale, out.dq)
+    return out
+
+
+def _amax_args(f: int, global_amax, device):
+    """(calibrated abs-max or None, scratch for a computed one or None)."""
+    if f != 0:
+        return None, None
+    if global_amax is not None:
+        _need(global_amax, "global_amax", torch.float32, 1)
+        _same_device(device, global_amax)
+        return global_amax, None
+    return None, torch.empty(1, dtype=torch.float32, device=device)
+
+
+def expert_quantize(x: torch.Tensor, plan: ExpertPlan, fmt="nvfp4", strategy="absmax", rot: int = 0,
+                    global_amax: Optional[torch.Tensor] = None,
+                    dq_dtype: Optional[torch.dtype] = None, out=None):
+    """quantize_mma() of bf16 tokens [tokens, cols] into the rows of their
+    choices; each token is quantized once. Returns a Quantized of
+    [plan.rows, cols] with MMA-layout scales (and dequantized values in
+    .dq, if dq_dtype or out.dq asks for them)."""
+    _need(x, "x", torch.bfloat16, None, None)
+    dev = x.device
+    _plan_args(plan, dev)
+    tokens, cols = x.shape
+    if plan.slots.shape[0] != tokens:
+        raise ValueError(f"x has {tokens} tokens, the plan {plan.slots.shape[0]}")
+    f = _fmt(fmt)
+    out = _quantized_out(out, plan.rows, cols, f, dq_dtype, dev)
+    amax, work = _amax_args(f, global_amax, dev)
+    _call("fp4q_expert_quantize", dev, x.data_ptr(), tokens, cols, plan.slots.shape[1],
+          plan.slots.data_ptr(), plan.rows, f, _strategy(strategy), rot, _ptr(amax),
+          _ptr(out.global_scale) if f == 0 else None, _ptr(work), out.codes.data_ptr(),
+          out.scales.data_ptr(), _ptr(out.dq), _DTYPES[out.dq.dtype] if out.dq is not None else 0)
+    return out
+
+
+def expert_weights(w: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0) -> ExpertWeights:
+    """Quantizes bf16 weights [experts, N, K] for expert_gemm, each expert with
+    its own scales (done once, when a model is loaded)."""
+    from . import Quantized, quantize_mma
+    _need(w, "w", torch.bfloat16, None, None, None)
+    experts, n, k = w.shape
+    f = _fmt(fmt)
+    dev = w.device
+    out = ExpertWeights(
+        torch.empty(experts, n, k // 2, dtype=torch.uint8, device=dev),
+        torch.zeros(experts, scale_bytes(n, k, f), dtype=torch.uint8, device=dev),
+        torch.empty(experts, dtype=torch.float32, device=dev) if f == 0 else None)
+    with torch.cuda.device(dev):
+        for e in range(experts):
+            gs = out.global_scale[e:e + 1] if f == 0 else None
+            quantize_mma(w[e], fmt, strategy, rot,
+                         out=Quantized(out.codes[e], out.scales[e], gs, None, None))
+    return out
+
+
+def expert_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scale: Optional[torch.Tensor],
+                w_codes: torch.Tensor, w_scales: torch.Tensor, w_global_scale: Optional[torch.Tensor],
+                plan: ExpertPlan, fmt="nvfp4", out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each row times its expert's weights, W4A4: [rows, K] x [experts, N, K]
+    -> [rows, N]. Operands as expert_quantize / glu_quantize and expert_weights
+    return them."""
+    f = _fmt(fmt)
+    _need(w_codes, "w_codes", torch.uint8, None, None, None)
+    experts, n, half = w_codes.shape
+    dev = w_codes.device
+    k = 2 * half
+    _plan_args(plan, dev)
+    rows = plan.rows
+    _need(a_codes, "a_codes", torch.uint8, rows, half)
+    _need(a_scales, "a_scales", torch.uint8, scale_bytes(rows, k, f))
+    _need(w_scales, "w_scales", torch.uint8, experts, scale_bytes(n, k, f))
+    _need(plan.counts, "plan.counts", torch.int32, experts)
+    _need(plan.starts, "plan.starts", torch.int32, experts + 1)
+    if f == 0:
+        _need(a_global_scale, "a_global_scale", torch.float32, 1)
+        _need(w_global_scale, "w_global_scale", torch.float32, experts)
+    else:
+        a_global_scale = w_global_scale = None
+    if out is None:
+        out = torch.empty(rows, n, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", (torch.float32, torch.bfloat16), rows, n)
+    _same_device(dev, a_codes, a_scales, a_global_scale, w_scales, w_global_scale, plan.counts,
+                 plan.starts, out)
+    choices = plan.slots.numel()
+    _call("fp4q_expert_gemm", dev, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_global_scale),
+          w_codes.data_ptr(), w_scales.data_ptr(), _ptr(w_global_scale), plan.counts.data_ptr(),
+          plan.starts.data_ptr(), experts, rows, n, k, f, -(-choices // experts), out.data_ptr(),
+          _DTYPES[out.dtype])
+    return out
+
+
+def glu_quantize(gu: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0,
+                 plan: Optional[ExpertPlan] = None, act: str = "silu",
+                 global_amax: Optional[torch.Tensor] = None,
+                 dq_dtype: Optional[torch.dtype] = None, out=None):
+    """Gated activation and quantize_mma() in one pass: gu bf16 [rows, 2 * cols]
+    (gate, then value) -> Quantized of act(gate) * value. With a plan only the
+    rows that hold a choice are taken, without one all rows."""
+    _need(gu, "gu", torch.bfloat16, None, None)
+    dev = gu.device
+    rows, cols = gu.shape[0], gu.shape[1] // 2
+    if gu.shape[1] % 2:
+        raise ValueError("gu must have an even number of columns")
+    if plan is not None:
+        _plan_args(plan, dev)
+        if plan.rows != rows:
+            raise ValueError(f"gu has {rows} rows, the plan {plan.rows}")
+    f = _fmt(fmt)
+    out = _quantized_out(out, rows, cols, f, dq_dtype, dev)
+    amax, work = _amax_args(f, global_amax, dev)
+    _call("fp4q_glu_quantize", dev, gu.data_ptr(), rows, cols,
+          plan.slots.data_ptr() if plan is not None else None,
+          plan.slots.numel() if plan is not None else rows, _act(act), f, _strategy(strategy), rot,
+          _ptr(amax), _ptr(out.global_scale) if f == 0 else None, _ptr(work), out.codes.data_ptr(),
+          out.scales.data_ptr(), _ptr(out.dq), _DTYPES[out.dq.dtype] if out.dq is not None else 0)
+    return out
+
+
+def glu_bwd(gu: torch.Tensor, dh: torch.Tensor, plan: Optional[ExpertPlan] = None, act: str = "silu",
+            rot: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of glu_quantize's gate and value (bf16 [rows, 2 * cols]) from
+    dh = dL/d(quantized values) bf16 [rows, cols], straight through the rounding."""
+    _need(gu, "gu", torch.bfloat16, None, None)
+    dev = gu.device
+    rows, cols = gu.shape[0], gu.shape[1] // 2
+    _need(dh, "dh", torch.bfloat16, rows, cols)
+    if gu.shape[1] % 2:
+        raise ValueError("gu must have an even number of columns")
+    if plan is not None:
+        _plan_args(plan, dev)
+        if plan.rows != rows:
+            raise ValueError(f"gu has {rows} rows, the plan {plan.rows}")
+    if out is None:
+        out = torch.empty_like(gu)
+    else:
+        _need(out, "out", torch.bfloat16, rows, 2 * cols)
+    _same_device(dev, dh, out)
+    _call("fp4q_glu_bwd", dev, gu.data_ptr(), dh.data_ptr(), rows, cols,
+          plan.slots.data_ptr() if plan is not None else None,
+          plan.slots.numel() if plan is not None else rows, _act(act), rot, out.data_ptr())
+    return out
+
+
+def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Tensor] = None,
+                   rot: int = 0, out_dtype: torch.dtype = torch.bfloat16,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: ones), then
+    the rotation. Without weights and with the forward's rot it is the
+    straight-through gradient of expert_quantize."""
+    _need(y, "y", (torch.float32, torch.bfloat16), plan.rows, None)
+    dev = y.device
+    _plan_args(plan, dev)
+    tokens, k = plan.slots.shape
+    cols = y.shape[1]
+    if weights is not None:
+        _need(weights, "weights", torch.float32, tokens, k)
+    if out is None:
+        out = torch.empty(tokens, cols, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", (torch.float32, torch.bfloat16), tokens, cols)
+    _same_device(dev, weights, out)
+    _call("fp4q_expert_combine", dev, y.data_ptr(), _DTYPES[y.dtype], plan.rows, cols,
+          plan.slots.data_ptr(), tokens, k, _ptr(weights), rot, out.data_ptr(), _DTYPES[out.dtype])
+    return out
+
+
+def expert_combine_bwd(g: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
+                       weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       want_dweights: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradients of expert_combine (rot 0) from g = dL/dout: (dy of y's type
+    and shape, dweights float32 [tokens, k] or None)."""
+    _need(y, "y", (torch.float32, torch.bfloat16), plan.rows, None)
+    dev = y.device
+    _plan_args(plan, dev)
+    tokens, k = plan.slots.shape
+    cols = y.shape[1]
+    _need(g, "g", (torch.float32, torch.bfloat16), tokens, cols)
+    if weights is not None:
+        _need(weights, "weights", torch.float32, tokens, k)
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _need(out, "out", y.dtype, plan.rows, cols)
+    dw = torch.empty(tokens, k, dtype=torch.float32, device=dev) if want_dweights else None
+    if dw is not None and cols == 0:
+        dw.zero_()
+    _same_device(dev, g, weights, out)
+    _call("fp4q_expert_combine_bwd", dev, g.data_ptr(), _DTYPES[g.dtype], y.data_ptr(),
+          _DTYPES[y.dtype], plan.rows, cols, plan.slots.data_ptr(), tokens, k, _ptr(weights),
+          out.data_ptr(), _ptr(dw))
+    return out, dw
