@@ -289,18 +289,31 @@ cudaError_t device_error_word(unsigned** p)
     return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp4q_device_errors);
 }
 
-bool make_byte_map(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_rows)
+static bool make_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int bytes,
+                     const void* base, int64_t width, int64_t rows, int box_width, int box_rows)
 {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr)
         return false;
-    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(width * bytes)};
+    cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_byte_map(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_rows)
+{
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, 1, base, row_bytes, rows, 128,
+                    box_rows);
+}
+
+bool make_word_map(CUtensorMap* map, const void* base, int64_t row_words, int64_t rows, int box_words,
+                   int box_rows)
+{
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, CU_TENSOR_MAP_SWIZZLE_NONE, 8, base, row_words, rows,
+                    box_words, box_rows);
 }
 
 }  // namespace fp4q

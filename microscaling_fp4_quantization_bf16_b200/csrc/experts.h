@@ -17,6 +17,9 @@ namespace fp4q {
 // box of 128 bytes x box_rows rows); false if the driver refuses it.
 cudaError_t device_error_word(unsigned** p);
 bool make_byte_map(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_rows);
+// The same for a matrix of 8-byte words without swizzle, a box of box_words x box_rows.
+bool make_word_map(CUtensorMap* map, const void* base, int64_t row_words, int64_t rows, int box_words,
+                   int box_rows);
 
 constexpr int kSegRows = 128;  // every expert's segment starts at a multiple of this
 
