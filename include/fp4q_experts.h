@@ -41,6 +41,8 @@ extern "C" {
 /* Limits: 1 <= k <= 64, 1 <= experts <= 1024, and padded rows below 2^31. */
 #define FP4Q_MAX_EXPERTS 1024
 #define FP4Q_MAX_CHOICES 64
+/* Floats of the abs-max scratch of fp4q_expert_quantize and fp4q_glu_quantize. */
+#define FP4Q_AMAX_WORK 1024
 
 /* Gate of the gated linear unit: a(g) = g * sigmoid(z(g)) with
  * SILU z = g; GELU_TANH z = 2 sqrt(2/pi) (g + 0.044715 g^3), which is
@@ -83,7 +85,7 @@ fp4q_status fp4q_expert_sort(const void* ids, int id_bytes, int64_t n, int64_t e
  *              take the abs-max of all of x (rotated; tokens without a choice
  *              included) in an extra pass. Ignored for MXFP4.
  * global_scale_out NVFP4: device float, receives s_g.
- * amax_work    device float of scratch, needed when fmt is NVFP4 and
+ * amax_work    FP4Q_AMAX_WORK device floats of scratch, needed when fmt is NVFP4 and
  *              global_amax_in is NULL; distinct from global_scale_out.
  * codes        uint8 [rows, cols/2].
  * mma_scales   fp4q_mma_scale_bytes(rows, cols, fmt) bytes in the layout of

@@ -92,14 +92,19 @@ def load(path: str = LIB_PATH):
     return _lib
 
 
-def call(name: str, *args) -> None:
+def fail(name: str, st: int) -> None:
+    """Raises the error of a status other than FP4Q_OK."""
     lib = load()
-    st = getattr(lib, name)(*args)
+    msg = lib.fp4q_status_string(st).decode()
+    if st == 6:
+        msg += f"; cudaError {lib.fp4q_last_cuda_error()}"
+    raise Fp4qError(name, st, msg)
+
+
+def call(name: str, *args) -> None:
+    st = getattr(load(), name)(*args)
     if st != 0:
-        msg = lib.fp4q_status_string(st).decode()
-        if st == 6:
-            msg += f"; cudaError {lib.fp4q_last_cuda_error()}"
-        raise Fp4qError(name, st, msg)
+        fail(name, st)
 
 
 def status(name: str, *args) -> int:

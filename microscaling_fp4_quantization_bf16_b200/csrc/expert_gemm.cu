@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(GTHREADS, 1)
 }
 
 template <bool PAIR, bool NV, bool F32>
-cudaError_t gemm_one(const uint8_t* a_codes, const uint8_t* w_codes, const ExpertGemmArgs& a, int sms,
-                     cudaStream_t st)
+cudaError_t gemm_one(const uint8_t* a_codes, const uint8_t* w_codes, const ExpertGemmArgs& a, int dev,
+                     int sms, cudaStream_t st)
 {
     using T = Tile<PAIR>;
     Maps maps = {};
@@ -603,8 +603,8 @@ cudaError_t gemm_one(const uint8_t* a_codes, const uint8_t* w_codes, const Exper
     if (!ok)
         return cudaErrorInvalidValue;
     auto kern = expert_gemm_kernel<PAIR, NV, F32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess)
+    static std::atomic<uint64_t> done{0};
+    if (cudaError_t e = allow_smem(kern, T::SMEM, dev, done))
         return e;
     if (!PAIR)
         return launch_pdl(kern, dim3((unsigned)sms), dim3(GTHREADS), T::SMEM, st, maps, a);
@@ -627,13 +627,13 @@ cudaError_t gemm_one(const uint8_t* a_codes, const uint8_t* w_codes, const Exper
 
 template <bool PAIR>
 cudaError_t gemm_type(bool nv, bool out32, const uint8_t* a_codes, const uint8_t* w_codes,
-                      const ExpertGemmArgs& a, int sms, cudaStream_t st)
+                      const ExpertGemmArgs& a, int dev, int sms, cudaStream_t st)
 {
     if (nv)
-        return out32 ? gemm_one<PAIR, true, true>(a_codes, w_codes, a, sms, st)
-                     : gemm_one<PAIR, true, false>(a_codes, w_codes, a, sms, st);
-    return out32 ? gemm_one<PAIR, false, true>(a_codes, w_codes, a, sms, st)
-                 : gemm_one<PAIR, false, false>(a_codes, w_codes, a, sms, st);
+        return out32 ? gemm_one<PAIR, true, true>(a_codes, w_codes, a, dev, sms, st)
+                     : gemm_one<PAIR, true, false>(a_codes, w_codes, a, dev, sms, st);
+    return out32 ? gemm_one<PAIR, false, true>(a_codes, w_codes, a, dev, sms, st)
+                 : gemm_one<PAIR, false, false>(a_codes, w_codes, a, dev, sms, st);
 }
 
 }  // namespace
@@ -648,8 +648,8 @@ cudaError_t launch_expert_gemm(bool nv, bool out32, int64_t mean_rows, const uin
     if (e != cudaSuccess)
         return e;
     if (mean_rows <= 128)
-        return gemm_type<false>(nv, out32, a_codes, w_codes, a, sms, st);
-    return gemm_type<true>(nv, out32, a_codes, w_codes, a, sms, st);
+        return gemm_type<false>(nv, out32, a_codes, w_codes, a, dev, sms, st);
+    return gemm_type<true>(nv, out32, a_codes, w_codes, a, dev, sms, st);
 }
 
 }  // namespace fp4q

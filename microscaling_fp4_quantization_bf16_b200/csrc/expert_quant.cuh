@@ -100,6 +100,56 @@ __device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, WarpStage
     return q;
 }
 
+// The tensor abs-max that build_scale_tables reads, from the maxima of the
+// abs-max pass's CTAs (every CTA takes their maximum itself: no launch
+// in between, no value to clear beforehand). Ends with a CTA barrier.
+__device__ __forceinline__ void join_amax(const RowQuantArgs& a, float& joined, QuantArgs& q)
+{
+    if (a.amax_parts == 0)  // uniform
+        return;
+    __shared__ unsigned top[QTHREADS / 32];
+    unsigned m = 0;
+    for (int i = threadIdx.x; i < a.amax_parts; i += QTHREADS)
+        m = max(m, __float_as_uint(a.amax[i]));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (threadIdx.x % 32 == 0)
+        top[threadIdx.x / 32] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < QTHREADS / 32; ++w)
+            m = max(m, top[w]);
+        joined = __uint_as_float(m);
+    }
+    __syncthreads();
+    q.amax = &joined;
+}
+
+// Writes the CTA's maximum of m (bits of non-negative floats).
+__device__ __forceinline__ void put_amax(const RowQuantArgs& a, unsigned m)
+{
+    __shared__ unsigned top[QTHREADS / 32];
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (threadIdx.x % 32 == 0)
+        top[threadIdx.x / 32] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < QTHREADS / 32; ++w)
+            m = max(m, top[w]);
+        a.amax_out[blockIdx.x] = __uint_as_float(m);
+    }
+}
+
+__device__ __forceinline__ unsigned seg_amax(const float (&y)[SEG])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < SEG; ++k)
+        m = fmaxf(m, fabsf(y[k]));
+    return __float_as_uint(m);
+}
+
 template <int STRAT>
 struct RowMinBlocks {
     static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : 5;
@@ -116,7 +166,8 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     __shared__ WarpStage<B> stage[QTHREADS / 32];
     const int lane = threadIdx.x & 31;
     WarpStage<B>& st = stage[threadIdx.x / 32];
-    const QuantArgs qa = stage_args<B>(a, st);
+    QuantArgs qa = stage_args<B>(a, st);
+    __shared__ float joined;
     const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
     auto fetch = [&](int64_t s, uint4 (&raw)[4]) {
 #pragma unroll
@@ -127,6 +178,7 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * QTHREADS;
     fetch(s, raw);
+    join_amax(a, joined, qa);
     build_scale_tables<STRAT>(tab, qa);
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step) {
         float y[SEG];
@@ -243,7 +295,9 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     __shared__ WarpStage<B> stage[QTHREADS / 32];
     const int lane = threadIdx.x & 31;
     WarpStage<B>& st = stage[threadIdx.x / 32];
-    const QuantArgs qa = stage_args<B>(a, st);
+    QuantArgs qa = stage_args<B>(a, st);
+    __shared__ float joined;
+    join_amax(a, joined, qa);
     build_scale_tables<STRAT>(tab, qa);
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += (int64_t)gridDim.x * QTHREADS) {
@@ -262,15 +316,19 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     }
 }
 
-// Launch of a row quantize kernel over the resident CTAs.
+// Launch of a row quantize kernel over the resident CTAs, at most `most`.
 template <class K>
-cudaError_t launch_rows(K kernel, const RowQuantArgs& a, cudaStream_t st)
+cudaError_t launch_rows(K kernel, const RowQuantArgs& a, cudaStream_t st, int64_t most = 0x7FFFFFFF,
+                        int* ctas = nullptr)
 {
     const int64_t nblk = (a.nseg + QTHREADS - 1) / QTHREADS;
     const int64_t res = resident_ctas(kernel);
     if (res < 0)
         return cudaErrorUnknown;
-    const int64_t grid = nblk < res ? nblk : res;
+    int64_t grid = nblk < res ? nblk : res;
+    grid = grid < most ? grid : most;
+    if (ctas != nullptr)
+        *ctas = (int)grid;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(QTHREADS), 0, st, a, nblk);
 }
 

@@ -19,25 +19,21 @@ __global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, int6
         float y[SEG];
         load_glu(a, s < a.nseg ? row_of(a, i, 0) : -1, (uint32_t)s - i * a.spr, y);
         rotate_seg<ROT>(y, lane);
-#pragma unroll
-        for (int k = 0; k < SEG; ++k)
-            m = max(m, __float_as_uint(fabsf(y[k])));
+        m = max(m, seg_amax(y));
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (lane == 0 && m != 0)
-        atomicMax(a.amax_out, m);  // a maximum does not depend on the order
+    put_amax(a, m);
 }
 
 }  // namespace
 
-cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, cudaStream_t st)
+cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, int* parts, cudaStream_t st)
 {
     switch (rot) {
-    case 0: return launch_rows(glu_amax_kernel<0>, a, st);
-    case 16: return launch_rows(glu_amax_kernel<16>, a, st);
-    case 32: return launch_rows(glu_amax_kernel<32>, a, st);
-    case 64: return launch_rows(glu_amax_kernel<64>, a, st);
-    case 128: return launch_rows(glu_amax_kernel<128>, a, st);
+    case 0: return launch_rows(glu_amax_kernel<0>, a, st, FP4Q_AMAX_WORK, parts);
+    case 16: return launch_rows(glu_amax_kernel<16>, a, st, FP4Q_AMAX_WORK, parts);
+    case 32: return launch_rows(glu_amax_kernel<32>, a, st, FP4Q_AMAX_WORK, parts);
+    case 64: return launch_rows(glu_amax_kernel<64>, a, st, FP4Q_AMAX_WORK, parts);
+    case 128: return launch_rows(glu_amax_kernel<128>, a, st, FP4Q_AMAX_WORK, parts);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -2,6 +2,7 @@
 // points (experts_api.cu and the expert_*.cu kernels).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -20,6 +21,20 @@ bool make_byte_map(CUtensorMap* map, const void* base, int64_t row_bytes, int64_
 // The same for a matrix of 8-byte words without swizzle, a box of box_words x box_rows.
 bool make_word_map(CUtensorMap* map, const void* base, int64_t row_words, int64_t rows, int box_words,
                    int box_rows);
+
+// Raises a kernel's dynamic shared memory limit, once per kernel (`done`, a
+// bit per device ordinal below 64) and device.
+template <class K>
+cudaError_t allow_smem(K kernel, size_t bytes, int dev, std::atomic<uint64_t>& done)
+{
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit != 0 && (done.load(std::memory_order_acquire) & bit))
+        return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 constexpr int kSegRows = 128;  // every expert's segment starts at a multiple of this
 
@@ -47,20 +62,24 @@ struct RowQuantArgs {
     int k;
     int64_t rows;           // rows of the outputs; slots outside are skipped
     int act;                // glu: fp4q_activation
-    const float* amax;      // NVFP4: device abs-max
+    const float* amax;      // NVFP4: device abs-max, or the parts' maxima
+    int amax_parts;         // 0: *amax is the abs-max; else their number
     float* sg_out;
     uint8_t* codes;
     uint8_t* scales;
     void* dq;
     int dq_kind;            // 0 none, 1 fp32, 2 bf16
     uint32_t keep;          // 0xFFFFFFFF, passed at run time (see encode_seg)
-    unsigned* amax_out;     // glu abs-max pass
+    float* amax_out;        // abs-max pass: one maximum of each CTA
 };
 // strat: KStrat of NVFP4 (block 16) or MXFP4 (block 32).
 cudaError_t launch_token_quant(int strat, int rot, const RowQuantArgs& a, cudaStream_t st);
 cudaError_t launch_glu_quant_nv(int strat, int rot, const RowQuantArgs& a, cudaStream_t st);
 cudaError_t launch_glu_quant_mx(int strat, int rot, const RowQuantArgs& a, cudaStream_t st);
-cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, cudaStream_t st);
+// The abs-max pass: maxima of the rotated tokens, or of the rotated gated
+// activation, into a.amax_out; their number (at most FP4Q_AMAX_WORK) into *parts.
+cudaError_t launch_token_amax(int rot, const RowQuantArgs& a, int* parts, cudaStream_t st);
+cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, int* parts, cudaStream_t st);
 
 struct GluBwdArgs {
     const uint16_t* gu;

@@ -71,6 +71,7 @@ RowQuantArgs row_args(const void* x, int64_t count, int64_t rows, int64_t cols, 
     a.rows = rows;
     a.act = act;
     a.amax = nullptr;
+    a.amax_parts = 0;
     a.sg_out = fmt == FP4Q_FMT_NVFP4 ? sg_out : nullptr;
     a.codes = codes;
     a.scales = scales;
@@ -163,10 +164,8 @@ fp4q_status fp4q_expert_quantize(const void* x, int64_t tokens, int64_t cols, in
     if (nv) {
         a.amax = global_amax_in;
         if (global_amax_in == nullptr) {
-            cudaError_t e = cudaMemsetAsync(amax_work, 0, sizeof(float), stream);
-            if (e == cudaSuccess)
-                e = launch_amax(a.x, n, rot, reinterpret_cast<unsigned*>(amax_work), stream);
-            if (e != cudaSuccess)
+            a.amax_out = amax_work;
+            if (cudaError_t e = launch_token_amax(rot, a, &a.amax_parts, stream))
                 return record_cuda_error(e);
             a.amax = amax_work;
         }
@@ -253,11 +252,8 @@ fp4q_status fp4q_glu_quantize(const void* gu, int64_t rows, int64_t cols, const 
         return record_cuda_error(launch_glu_quant_mx(strat_id(fmt, strat), rot, a, stream));
     a.amax = global_amax_in;
     if (global_amax_in == nullptr) {
-        cudaError_t e = cudaMemsetAsync(amax_work, 0, sizeof(float), stream);
-        a.amax_out = reinterpret_cast<unsigned*>(amax_work);
-        if (e == cudaSuccess)
-            e = launch_glu_amax(rot, a, stream);
-        if (e != cudaSuccess)
+        a.amax_out = amax_work;
+        if (cudaError_t e = launch_glu_amax(rot, a, &a.amax_parts, stream))
             return record_cuda_error(e);
         a.amax = amax_work;
     }

@@ -27,6 +27,7 @@ from . import _abi
 
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 SEGMENT_ROWS = 128
+AMAX_WORK = 1024
 _FORMATS = {"nvfp4": 0, "mxfp4": 1}
 _STRATEGIES = {"absmax": 0, "prevent_zero": 1, "four_over_six": 2, "brute_force": 3}
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -51,6 +52,12 @@ class ExpertWeights:
 
 def _need(t, name: str, dtype, *shape) -> None:
     """t is a contiguous CUDA tensor of dtype (or one of several) and shape (None: any)."""
+    try:
+        if (t.is_cuda and (t.dtype is dtype or t.dtype in dtype) and t.is_contiguous()
+                and (not shape or t.shape == shape)):
+            return
+    except (AttributeError, TypeError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
@@ -60,6 +67,15 @@ def _need(t, name: str, dtype, *shape) -> None:
     if shape and (t.dim() != len(shape) or any(s is not None and s != d
                                                for s, d in zip(shape, t.shape))):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _matrix(t, name: str, dtype):
+    """The shape of t, a contiguous CUDA matrix of dtype (or one of several)."""
+    _need(t, name, dtype)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(shape)}")
+    return shape
 
 
 def _fmt(fmt) -> int:
@@ -82,13 +98,26 @@ def _act(act) -> int:
     return ACTIVATIONS[act]
 
 
+_bound = {}  # entry points of the loaded library, by name
+
+
+def _entry(name: str):
+    fn = _bound.get(name)
+    if fn is None:
+        fn = _bound[name] = getattr(_abi.load(), name)
+    return fn
+
+
 def _call(name: str, device: torch.device, *args) -> None:
     """Calls an entry point on the current stream of `device`."""
-    if device.index == torch.cuda.current_device():
-        _abi.call(name, *args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _abi.call(name, *args, torch.cuda.current_stream().cuda_stream)
+            status = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _abi.fail(name, status)
 
 
 def _same_device(device, *tensors) -> None:
@@ -102,7 +131,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _plan_args(plan: ExpertPlan, device) -> None:
-    _need(plan.slots, "plan.slots", torch.int32, None, None)
+    _matrix(plan.slots, "plan.slots", torch.int32)
     _same_device(device, plan.slots)
     if plan.rows < 0 or plan.rows % SEGMENT_ROWS:
         raise ValueError(f"plan.rows must be a multiple of {SEGMENT_ROWS}, got {plan.rows}")
@@ -116,7 +145,7 @@ def scale_bytes(rows: int, cols: int, fmt="nvfp4") -> int:
 
 def expert_rows(choices: int, experts: int) -> int:
     """Rows of the padded layout that hold any routing of `choices` choices."""
-    rows = _abi.load().fp4q_expert_rows(choices, experts)
+    rows = _entry("fp4q_expert_rows")(choices, experts)
     if rows < 0:
         raise ValueError(f"no row layout for {choices} choices among {experts} experts")
     return rows
@@ -127,24 +156,25 @@ def expert_sort(ids: torch.Tensor, experts: int, rows: Optional[int] = None,
     """Sorts the router's choices ids (int32 or int64 [tokens, k]) by expert,
     stably. An id outside 0 .. experts-1 drops the choice. rows: rows of the
     layout, at least the default expert_rows(tokens * k, experts)."""
-    _need(ids, "ids", (torch.int32, torch.int64), None, None)
-    lib = _abi.load()
+    _matrix(ids, "ids", (torch.int32, torch.int64))
+    dev = ids.device
     n = ids.numel()
     least = expert_rows(n, experts)
     if out is None:
-        out = ExpertPlan(ids.new_empty(experts, dtype=torch.int32),
-                         ids.new_empty(experts + 1, dtype=torch.int32),
-                         ids.new_empty(ids.shape, dtype=torch.int32), least if rows is None else rows)
+        out = ExpertPlan(torch.empty(experts, dtype=torch.int32, device=dev),
+                         torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                         torch.empty(ids.shape, dtype=torch.int32, device=dev),
+                         least if rows is None else rows)
     else:
         _need(out.counts, "out.counts", torch.int32, experts)
         _need(out.starts, "out.starts", torch.int32, experts + 1)
         _need(out.slots, "out.slots", torch.int32, *ids.shape)
-        _same_device(ids.device, out.counts, out.starts, out.slots)
+        _same_device(dev, out.counts, out.starts, out.slots)
     if out.rows < least or out.rows % SEGMENT_ROWS:
         raise ValueError(f"rows must be a multiple of {SEGMENT_ROWS} and at least {least}, got {out.rows}")
-    size = lib.fp4q_expert_sort_work(n, experts)
-    work = ids.new_empty(size // 4, dtype=torch.int32) if size else None
-    _call("fp4q_expert_sort", ids.device, ids.data_ptr(), ids.element_size(), n, experts,
+    size = _entry("fp4q_expert_sort_work")(n, experts)
+    work = torch.empty(size // 4, dtype=torch.int32, device=dev) if size else None
+    _call("fp4q_expert_sort", dev, ids.data_ptr(), ids.element_size(), n, experts,
           out.counts.data_ptr(), out.starts.data_ptr(), out.slots.data_ptr(), _ptr(work))
     return out
 
@@ -177,7 +207,7 @@ def _amax_args(f: int, global_amax, device):
         _need(global_amax, "global_amax", torch.float32, 1)
         _same_device(device, global_amax)
         return global_amax, None
-    return None, torch.empty(1, dtype=torch.float32, device=device)
+    return None, torch.empty(AMAX_WORK, dtype=torch.float32, device=device)
 
 
 def expert_quantize(x: torch.Tensor, plan: ExpertPlan, fmt="nvfp4", strategy="absmax", rot: int = 0,
@@ -187,10 +217,9 @@ def expert_quantize(x: torch.Tensor, plan: ExpertPlan, fmt="nvfp4", strategy="ab
     choices; each token is quantized once. Returns a Quantized of
     [plan.rows, cols] with MMA-layout scales (and dequantized values in
     .dq, if dq_dtype or out.dq asks for them)."""
-    _need(x, "x", torch.bfloat16, None, None)
+    tokens, cols = _matrix(x, "x", torch.bfloat16)
     dev = x.device
     _plan_args(plan, dev)
-    tokens, cols = x.shape
     if plan.slots.shape[0] != tokens:
         raise ValueError(f"x has {tokens} tokens, the plan {plan.slots.shape[0]}")
     f = _fmt(fmt)
@@ -207,7 +236,9 @@ def expert_weights(w: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0
     """Quantizes bf16 weights [experts, N, K] for expert_gemm, each expert with
     its own scales (done once, when a model is loaded)."""
     from . import Quantized, quantize_mma
-    _need(w, "w", torch.bfloat16, None, None, None)
+    _need(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError(f"w must have shape [experts, N, K], got {tuple(w.shape)}")
     experts, n, k = w.shape
     f = _fmt(fmt)
     dev = w.device
@@ -231,7 +262,9 @@ def expert_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scale: O
     -> [rows, N]. Operands as expert_quantize / glu_quantize and expert_weights
     return them."""
     f = _fmt(fmt)
-    _need(w_codes, "w_codes", torch.uint8, None, None, None)
+    _need(w_codes, "w_codes", torch.uint8)
+    if w_codes.dim() != 3:
+        raise ValueError(f"w_codes must have shape [experts, N, K/2], got {tuple(w_codes.shape)}")
     experts, n, half = w_codes.shape
     dev = w_codes.device
     k = 2 * half
@@ -268,10 +301,9 @@ def glu_quantize(gu: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0,
     """Gated activation and quantize_mma() in one pass: gu bf16 [rows, 2 * cols]
     (gate, then value) -> Quantized of act(gate) * value. With a plan only the
     rows that hold a choice are taken, without one all rows."""
-    _need(gu, "gu", torch.bfloat16, None, None)
-    dev = gu.device
-    rows, cols = gu.shape[0], gu.shape[1] // 2
-    if gu.shape[1] % 2:
+    rows, cols = _matrix(gu, "gu", torch.bfloat16)
+    dev, cols, odd = gu.device, cols // 2, cols % 2
+    if odd:
         raise ValueError("gu must have an even number of columns")
     if plan is not None:
         _plan_args(plan, dev)
@@ -292,11 +324,10 @@ def glu_bwd(gu: torch.Tensor, dh: torch.Tensor, plan: Optional[ExpertPlan] = Non
             rot: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of glu_quantize's gate and value (bf16 [rows, 2 * cols]) from
     dh = dL/d(quantized values) bf16 [rows, cols], straight through the rounding."""
-    _need(gu, "gu", torch.bfloat16, None, None)
-    dev = gu.device
-    rows, cols = gu.shape[0], gu.shape[1] // 2
+    rows, cols = _matrix(gu, "gu", torch.bfloat16)
+    dev, cols, odd = gu.device, cols // 2, cols % 2
     _need(dh, "dh", torch.bfloat16, rows, cols)
-    if gu.shape[1] % 2:
+    if odd:
         raise ValueError("gu must have an even number of columns")
     if plan is not None:
         _plan_args(plan, dev)
@@ -319,11 +350,12 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
     """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: ones), then
     the rotation. Without weights and with the forward's rot it is the
     straight-through gradient of expert_quantize."""
-    _need(y, "y", (torch.float32, torch.bfloat16), plan.rows, None)
+    rows, cols = _matrix(y, "y", (torch.float32, torch.bfloat16))
     dev = y.device
     _plan_args(plan, dev)
+    if rows != plan.rows:
+        raise ValueError(f"y has {rows} rows, the plan {plan.rows}")
     tokens, k = plan.slots.shape
-    cols = y.shape[1]
     if weights is not None:
         _need(weights, "weights", torch.float32, tokens, k)
     if out is None:
@@ -341,11 +373,12 @@ def expert_combine_bwd(g: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
                        want_dweights: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Gradients of expert_combine (rot 0) from g = dL/dout: (dy of y's type
     and shape, dweights float32 [tokens, k] or None)."""
-    _need(y, "y", (torch.float32, torch.bfloat16), plan.rows, None)
+    rows, cols = _matrix(y, "y", (torch.float32, torch.bfloat16))
     dev = y.device
     _plan_args(plan, dev)
+    if rows != plan.rows:
+        raise ValueError(f"y has {rows} rows, the plan {plan.rows}")
     tokens, k = plan.slots.shape
-    cols = y.shape[1]
     _need(g, "g", (torch.float32, torch.bfloat16), tokens, cols)
     if weights is not None:
         _need(weights, "weights", torch.float32, tokens, k)
