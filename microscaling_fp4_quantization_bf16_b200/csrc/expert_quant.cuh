@@ -3,11 +3,16 @@
 //
 // Arithmetic: process_segment of quant_kernel.cuh, one thread to a 32-element
 // segment, so codes, scales and values are bit for bit those of the plain
-// quantizer. It writes into a small shared-memory buffer of the warp instead
-// of global memory (its pointers are generic); from there a token's segment goes to
-// each of its k rows, so a token is read and quantized once however many
-// experts take it, and the 64-byte (bf16) or 128-byte (fp32) pieces of the
-// values leave as 512 contiguous bytes a warp.
+// quantizer. A token is read and quantized once however many experts take it.
+//
+// Memory: each warp brings its next 32 segments (2 KB of bf16, twice that for
+// gate and value) into shared memory with 16-byte asynchronous copies while it
+// works on the current ones, 512 contiguous bytes a copy instruction (chunk c of
+// segment s at slot c ^ (s / 2 % 4) of its four, so that reading a segment a lane is free of
+// bank conflicts too). No register holds a byte in flight. process_segment writes its codes and scale bytes
+// to the warp's buffer (its pointers are generic); from there a segment goes to each of
+// its token's rows. The dequantized values are formed from the staged codes by
+// the lane that stores them, again 512 contiguous bytes an instruction.
 #pragma once
 
 #include "experts.h"
@@ -15,41 +20,94 @@
 
 namespace fp4q {
 
-// One warp's staging buffer: 32 segments' codes, scale bytes and values.
-template <int B>
+// One warp's shared memory: two buffers of 32 segments of IN bf16 inputs in
+// chunks of 8 values, and their codes and scale bytes.
+template <int B, int IN>
 struct WarpStage {
+    uint4 in[2][IN][32 * 4];
     uint4 codes[32];
-    uint8_t scales[32 * (SEG / B)];
-    __align__(16) uint8_t dq[32 * SEG * sizeof(float)];
+    __align__(4) uint8_t scales[32 * (SEG / B)];
 };
 
-// The destination rows of one segment's choice j; -1 where there is none.
+// Slot of chunk c (segment c / 4, part c % 4) in a buffer.
+__device__ __forceinline__ int slot_of(int c) { return c ^ ((c >> 3) & 3); }
+
+__device__ __forceinline__ void copy16(uint4* dst, const uint4* src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// Where this lane's segment lies: segment p of token (or taken row) i. one: the warp's 32
+// segments all lie in the same row, so that addresses are a base of the warp plus the lane
+// (a shuffle and a 64-bit product per chunk otherwise).
+struct Place {
+    uint32_t i, p;
+    bool live, one;
+};
+
+__device__ __forceinline__ Place place_of(const RowQuantArgs& a, int64_t s, int lane)
+{
+    const uint32_t s0 = (uint32_t)(s - lane), i0 = s0 / a.spr, p0 = s0 - i0 * a.spr;
+    Place at{i0, p0 + lane, s < a.nseg, p0 + 32 <= a.spr};
+    while (at.p >= a.spr) {  // rows shorter than 32 segments: a warp spans several
+        at.p -= a.spr;
+        ++at.i;
+    }
+    return at;
+}
+
+// The destination row of choice j of token i; -1 where there is none.
 __device__ __forceinline__ int32_t row_of(const RowQuantArgs& a, int64_t i, int j)
 {
-    int32_t r = a.slots == nullptr ? (int32_t)i : a.slots[i * a.k + j];
+    const int32_t r = a.slots == nullptr ? (int32_t)i : a.slots[i * a.k + j];
     return r < a.rows ? r : -1;
 }
 
-// Copies the staged segments of a warp to their rows. i, p: token (or taken
-// row) and segment within it of this lane; live: the lane has a segment. All lanes take part.
-template <int B>
-__device__ __forceinline__ void store_rows(const RowQuantArgs& a, const WarpStage<B>& st, int lane,
-                                           int64_t i, uint32_t p, bool live)
+// Copies the staged segments of a warp to the rows row(j), j < k, of this lane's
+// segment (-1: none). All lanes take part.
+template <int B, int STRAT, class Rows>
+__device__ __forceinline__ void store_rows(const RowQuantArgs& a, const uint4* codes,
+                                           const uint8_t* scales, const ScaleTables<STRAT>& tab,
+                                           int lane, const Place& at, Rows row)
 {
     constexpr int NB = SEG / B;      // blocks of a segment
     constexpr int QUAD = 4 / NB;     // segments of a 4-block group
-    const uint4 q = st.codes[lane];
+    const uint4 q = codes[lane];
     // Segments per row a multiple of QUAD: the groups of 4 blocks lie inside
     // the warp, and the first lane of each writes its 4 bytes at once.
     const bool whole = a.spr % QUAD == 0;
     uint32_t quad = 0;
     if (whole && lane % QUAD == 0)
-        quad = *reinterpret_cast<const uint32_t*>(st.scales + lane * NB);
+        quad = *reinterpret_cast<const uint32_t*>(scales + lane * NB);
+    uint4 o[4];
+    if (a.dq_kind == 2) {
+        // bf16 values: chunk 32 c + lane is 8 values of segment 8 c + lane / 4
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t byte = scales[(8 * c + lane / 4) * NB + lane % 4 * 8 / B];
+            float S, v[8];
+            if constexpr (is_mx_strat(STRAT))
+                S = pow2f((int)byte - 127);
+            else
+                S = tab.S[byte];
+            e2m1_unpack8(reinterpret_cast<const uint32_t*>(codes)[32 * c + lane], v);
+            o[c].x = pack_bf16x2(__fmul_rn(v[0], S), __fmul_rn(v[1], S));
+            o[c].y = pack_bf16x2(__fmul_rn(v[2], S), __fmul_rn(v[3], S));
+            o[c].z = pack_bf16x2(__fmul_rn(v[4], S), __fmul_rn(v[5], S));
+            o[c].w = pack_bf16x2(__fmul_rn(v[6], S), __fmul_rn(v[7], S));
+        }
+    }
     for (int j = 0; j < a.k; ++j) {
-        const int32_t r = live ? row_of(a, i, j) : -1;
+        const int32_t r = row(j);
+        const int64_t seg = (int64_t)r * a.spr + at.p;
         if (r >= 0) {
-            *reinterpret_cast<uint4*>(a.codes + ((int64_t)r * a.spr + p) * (SEG / 2)) = q;
-            const uint32_t kb = p * NB;
+            reinterpret_cast<uint4*>(a.codes)[seg] = q;
+            const uint32_t kb = at.p * NB;
             uint8_t* dst = a.scales + ((int64_t)(r >> 7) * a.atoms_k + (kb >> 2)) * 512 +
                            16 * (r & 31) + 4 * ((r >> 5) & 3);
             if (whole) {
@@ -58,42 +116,64 @@ __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const WarpStag
             } else {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    dst[(kb & 3) + b] = st.scales[lane * NB + b];
-                if (p == a.spr - 1)  // padding blocks of the row's last group
+                    dst[(kb & 3) + b] = scales[lane * NB + b];
+                if (at.p == a.spr - 1)  // padding blocks of the row's last group
                     for (uint32_t b = (kb & 3) + NB; b < 4; ++b)
                         dst[b] = 0;
             }
         }
-        if (a.dq_kind == 0)  // uniform
-            continue;
-        const int bytes = a.dq_kind == 1 ? 4 * SEG : 2 * SEG;  // of a segment's values
-        const int per = bytes / 16;
-        for (int c = lane; c < 32 * per; c += 32) {
-            const int sl = c / per;
-            const int32_t rs = __shfl_sync(0xFFFFFFFFu, r, sl);
-            const uint32_t ps = __shfl_sync(0xFFFFFFFFu, p, sl);
-            if (rs >= 0)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dq) +
-                                          ((int64_t)rs * a.spr + ps) * bytes + 16 * (c % per)) =
-                    *reinterpret_cast<const uint4*>(st.dq + 16 * c);
+        if (a.dq_kind == 2) {
+            if (at.one) {
+                if (r >= 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.dq) + (seg - lane) * 4 + lane;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        dst[32 * c] = o[c];
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int32_t rs = __shfl_sync(0xFFFFFFFFu, r, 8 * c + lane / 4);
+                    const uint32_t ps = __shfl_sync(0xFFFFFFFFu, at.p, 8 * c + lane / 4);
+                    if (rs >= 0)
+                        reinterpret_cast<uint4*>(a.dq)[((int64_t)rs * a.spr + ps) * 4 + lane % 4] = o[c];
+                }
+            }
+        } else if (a.dq_kind == 1 && r >= 0) {
+            // fp32 values (for checks and calibration on small layers): each lane its segment
+            float4* dst = reinterpret_cast<float4*>(a.dq) + seg * (SEG / 4);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t byte = scales[lane * NB + c * 8 / B];
+                float S, v[8];
+                if constexpr (is_mx_strat(STRAT))
+                    S = pow2f((int)byte - 127);
+                else
+                    S = tab.S[byte];
+                e2m1_unpack8(w[c], v);
+                dst[2 * c] = make_float4(__fmul_rn(v[0], S), __fmul_rn(v[1], S), __fmul_rn(v[2], S),
+                                         __fmul_rn(v[3], S));
+                dst[2 * c + 1] = make_float4(__fmul_rn(v[4], S), __fmul_rn(v[5], S), __fmul_rn(v[6], S),
+                                             __fmul_rn(v[7], S));
+            }
         }
     }
 }
 
-// The staging buffer as the output of process_segment.
-template <int B>
-__device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, WarpStage<B>& st)
+// The warp's buffer as the output of process_segment.
+__device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, uint4* codes, uint8_t* scales)
 {
     QuantArgs q;
     q.x = nullptr;
     q.n = 0;
     q.amax = a.amax;
     q.sg_out = a.sg_out;
-    q.codes = reinterpret_cast<uint8_t*>(st.codes);
-    q.scales = st.scales;
+    q.codes = reinterpret_cast<uint8_t*>(codes);
+    q.scales = scales;
     q.mse = nullptr;
-    q.dq = st.dq;
-    q.dq_kind = a.dq_kind;
+    q.dq = nullptr;
+    q.dq_kind = 0;
     q.keep = a.keep;
     q.mma_spr = 0;
     q.mma_atoms_k = 0;
@@ -150,49 +230,73 @@ __device__ __forceinline__ unsigned seg_amax(const float (&y)[SEG])
     return __float_as_uint(m);
 }
 
+// CTAs per SM that the registers are held to: searches as the compiler likes.
 template <int STRAT>
 struct RowMinBlocks {
     static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : 5;
 };
 
-// Tokens: segment s of x is segment s % spr of token s / spr. Persistent CTAs;
-// the next tile's loads are in flight during this tile's arithmetic.
+// ---------------------------------------------------------------- tokens
+
+// Starts the copies of the warp's 32 segments from segment s0 of x.
+__device__ __forceinline__ void fetch_tokens(const RowQuantArgs& a, int64_t s0, int lane, uint4* in)
+{
+    const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t at = s0 * 4 + 32 * c + lane;
+        const bool real = at < 4 * a.nseg;
+        copy16(in + slot_of(32 * c + lane), x4 + (real ? at : 0), real);
+    }
+}
+
+// Segment s of x is segment s % spr of token s / spr. Persistent CTAs.
 template <int B, int ROT, int STRAT>
 __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     token_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B> stage[QTHREADS / 32];
-    const int lane = threadIdx.x & 31;
-    WarpStage<B>& st = stage[threadIdx.x / 32];
-    QuantArgs qa = stage_args<B>(a, st);
+    __shared__ WarpStage<B, 1> stage[QTHREADS / 32];
     __shared__ float joined;
-    const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
-    auto fetch = [&](int64_t s, uint4 (&raw)[4]) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            raw[k] = s < a.nseg ? ldg_stream(x4 + 4 * s + k) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    uint4 raw[4];
+    const int lane = threadIdx.x & 31;
+    WarpStage<B, 1>& st = stage[threadIdx.x / 32];
+    QuantArgs qa = stage_args(a, st.codes, st.scales);
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * QTHREADS;
-    fetch(s, raw);
+    fetch_tokens(a, s - lane, lane, st.in[0][0]);
+    copies_commit();
     join_amax(a, joined, qa);
     build_scale_tables<STRAT>(tab, qa);
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step) {
-        float y[SEG];
-        unpack_seg<!is_mx_strat(STRAT)>(raw, y);
+    int buf = 0;
+    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1) {
         if (t + gridDim.x < ntiles)
-            fetch(s + step, raw);
+            fetch_tokens(a, s + step - lane, lane, st.in[buf ^ 1][0]);
+        copies_commit();
+        copies_wait_but_one();
+        __syncwarp();
         if (s - lane < a.nseg) {  // warp-uniform
+            const Place at = place_of(a, s, lane);
+            // the rows of the first 32 choices, one a lane, on their way during the arithmetic
+            int32_t mine = -1;
+            if (at.one && lane < a.k)
+                mine = row_of(a, at.i, lane);
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = st.in[buf][0][slot_of(4 * lane + k)];
+            float y[SEG];
+            unpack_seg<!is_mx_strat(STRAT)>(v, y);
             rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
             process_segment<B, STRAT, ROT>(y, lane, SEG, qa, tab);
             __syncwarp();
-            const uint32_t i = (uint32_t)s / a.spr;
-            store_rows<B>(a, st, lane, i, (uint32_t)s - i * a.spr, s < a.nseg);
-            __syncwarp();
+            store_rows<B, STRAT>(a, st.codes, st.scales, tab, lane, at, [&](int j) {
+                if (at.one && j < 32)
+                    return __shfl_sync(0xFFFFFFFFu, mine, j);
+                return at.live ? row_of(a, at.i, j) : -1;
+            });
         }
+        __syncwarp();
     }
 }
 
@@ -200,23 +304,28 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 
 // h = bf16(fp32(g u sigmoid(z))) from its real value: 64 bits, one rounding to
 // fp32, one to bf16. Only pairs whose rounding the fp32 path cannot decide come here.
-static __device__ __noinline__ uint32_t glu_pair_exact(uint32_t g2, uint32_t u2, int act)
+template <int ACT>
+static __device__ __noinline__ uint32_t glu_pair_exact(uint32_t g2, uint32_t u2)
 {
     uint32_t out = 0;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        const double g = (double)__uint_as_float(k ? g2 & 0xFFFF0000u : g2 << 16);
-        const double u = (double)__uint_as_float(k ? u2 & 0xFFFF0000u : u2 << 16);
-        const double z = act == FP4Q_ACT_GELU_TANH
-                             ? 1.5957691216057307612 * (g + 0.044715 * g * g * g)
-                             : g;
-        const float h = (float)(g * u / (1.0 + exp(-z)));
-        out |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(h)) << (16 * k);
+        const uint32_t gb = k ? g2 & 0xFFFF0000u : g2 << 16, ub = k ? u2 & 0xFFFF0000u : u2 << 16;
+        uint32_t h = (gb ^ ub) & 0x80000000u;  // a zero factor gives a signed zero
+        if (((gb << 1) != 0) && ((ub << 1) != 0)) {
+            const double g = (double)__uint_as_float(gb), u = (double)__uint_as_float(ub);
+            const double z = ACT == FP4Q_ACT_GELU_TANH
+                                 ? 1.5957691216057307612 * (g + 0.044715 * g * g * g)
+                                 : g;
+            h = __float_as_uint((float)(g * u / (1.0 + exp(-z))));
+        }
+        out |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(h))) << (16 * k);
     }
     return out;
 }
 
-// Two values of h as packed bf16, from packed bf16 gates and values.
+// Two values of h as packed bf16, from packed bf16 gates and values, and whether
+// they are certain.
 //
 // v = (g u) / (1 + 2^(-z log2 e)) in fp32 with the hardware's 2^x and 1/x is
 // within E |v| of the real value: 2^x is off by 2^-22.5 and its argument
@@ -225,95 +334,169 @@ static __device__ __noinline__ uint32_t glu_pair_exact(uint32_t g2, uint32_t u2,
 // E = 2^-20 + 2^-21 max(-z, 0) covers all of it. The ends v (1 -+ E) of that
 // bracket round to the same bf16 in all but about one pair in a thousand; those, and
 // whatever leaves the range in which relative errors hold, are formed in 64 bits.
-__device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, bool gelu, int act)
+// (Both halves of a pair run on packed fp32 operations.)
+template <int ACT>
+__device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, bool& certain)
 {
-    uint32_t lo[2];
-    bool ok = true;
-    float b[2][2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float g = k ? bf_hi(g2) : bf_lo(g2);
-        const float u = k ? bf_hi(u2) : bf_lo(u2);
-        float z = g;
-        if (gelu)
-            z = (1.5957691216f * g) * __fmaf_rn(0.044715f * g, g, 1.0f);
-        float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950409f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-        const float v = (g * u) * r;
-        const float err = __fmaf_rn(fmaxf(-z, 0.0f), 0x1p-21f, 0x1p-20f);
-        b[0][k] = __fmaf_rn(v, -err, v);
-        b[1][k] = __fmaf_rn(v, err, v);
-        // z > -60 keeps 2^x and its reciprocal in range, |v| > 2^-100 the products
-        // (g u and v differ by a factor above 2^-88); a zero factor is exact
-        ok = ok && z > -60.0f && (fabsf(v) > 0x1p-100f || g == 0.0f || u == 0.0f);
-    }
-    lo[0] = pack_bf16x2(b[0][0], b[0][1]);
-    lo[1] = pack_bf16x2(b[1][0], b[1][1]);
-    if (ok && lo[0] == lo[1])
-        return lo[0];
-    return glu_pair_exact(g2, u2, act);
+    const f32x2 g = pk2(bf_lo(g2), bf_hi<true>(g2)), u = pk2(bf_lo(u2), bf_hi<true>(u2));
+    f32x2 z = g;
+    if constexpr (ACT == FP4Q_ACT_GELU_TANH)
+        z = mul2(mul2(g, pk2(1.5957691216f, 1.5957691216f)),
+                 fma2(mul2(g, pk2(0.044715f, 0.044715f)), g, pk2(1.0f, 1.0f)));
+    float z0, z1, t0, t1, r0, r1;
+    upk2(mul2(z, pk2(-1.4426950409f, -1.4426950409f)), t0, t1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
+    upk2(add2(pk2(t0, t1), pk2(1.0f, 1.0f)), t0, t1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(t0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(t1));
+    const f32x2 v = mul2(mul2(g, u), pk2(r0, r1));
+    upk2(z, z0, z1);
+    const f32x2 err = fma2(pk2(fminf(z0, 0.0f), fminf(z1, 0.0f)), pk2(-0x1p-21f, -0x1p-21f),
+                           pk2(0x1p-20f, 0x1p-20f));
+    float lo0, lo1, hi0, hi1, v0, v1;
+    const f32x2 d = mul2(v, err);
+    upk2(add2(v, d), hi0, hi1);
+    upk2(sub2(v, d), lo0, lo1);
+    upk2(v, v0, v1);
+    const uint32_t hi = pack_bf16x2(hi0, hi1);
+    // z > -60 keeps 2^x and its reciprocal in range, |v| > 2^-100 the products
+    // (g u and v differ by a factor below 2^88); NaN fails too
+    certain = fminf(z0, z1) > -60.0f && fminf(fabsf(v0), fabsf(v1)) > 0x1p-100f &&
+              pack_bf16x2(lo0, lo1) == hi;
+    return hi;
 }
 
-// The 32 values of one segment of h, widened; row < 0 gives zeros.
-__device__ __forceinline__ void load_glu(const RowQuantArgs& a, int64_t row, uint32_t p, float (&y)[SEG])
+// This lane's segment of h, widened, from its gates and values in shared memory. The pairs
+// run without a branch between them; the uncertain ones follow one by one, patched through the gates' slots.
+template <int ACT>
+__device__ __forceinline__ void glu_segment(uint4* gate, const uint4* value, int lane, float (&y)[SEG])
 {
-    if (row < 0) {
-#pragma unroll
-        for (int i = 0; i < SEG; ++i)
-            y[i] = 0.0f;
-        return;
-    }
-    const uint4* g4 = reinterpret_cast<const uint4*>(a.x) + ((int64_t)row * 2 * a.spr + p) * 4;
-    const uint4* u4 = g4 + (int64_t)a.spr * 4;
-    uint4 g[4], u[4];
+    uint4 h[4];
+    uint32_t redo = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        g[k] = ldg_stream(g4 + k);
-        u[k] = ldg_stream(u4 + k);
+        const uint4 g = gate[slot_of(4 * lane + k)], u = value[slot_of(4 * lane + k)];
+        bool c0, c1, c2, c3;
+        h[k].x = glu_pair<ACT>(g.x, u.x, c0);
+        h[k].y = glu_pair<ACT>(g.y, u.y, c1);
+        h[k].z = glu_pair<ACT>(g.z, u.z, c2);
+        h[k].w = glu_pair<ACT>(g.w, u.w, c3);
+        redo |= (c0 ? 0u : 1u << (4 * k)) | (c1 ? 0u : 2u << (4 * k)) | (c2 ? 0u : 4u << (4 * k)) |
+                (c3 ? 0u : 8u << (4 * k));
     }
-    const bool gelu = a.act == FP4Q_ACT_GELU_TANH;
+    if (redo != 0) {
+        uint32_t* gw = reinterpret_cast<uint32_t*>(gate);
+        const uint32_t* uw = reinterpret_cast<const uint32_t*>(value);
+        for (uint32_t m = redo; m != 0; m &= m - 1) {
+            const int pair = __ffs(m) - 1;
+            const int at = slot_of(4 * lane + pair / 4) * 4 + pair % 4;
+            gw[at] = glu_pair_exact<ACT>(gw[at], uw[at]);
+        }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
-        const uint32_t uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        for (int k = 0; k < 4; ++k) {
+            const uint4 w = gate[slot_of(4 * lane + k)];
+            h[k].x = redo & (1u << (4 * k)) ? w.x : h[k].x;
+            h[k].y = redo & (2u << (4 * k)) ? w.y : h[k].y;
+            h[k].z = redo & (4u << (4 * k)) ? w.z : h[k].z;
+            h[k].w = redo & (8u << (4 * k)) ? w.w : h[k].w;
+        }
+    }
+    unpack_seg<true>(h, y);
+}
+
+// Starts the copies of the warp's 32 segments of gate and value. row: the
+// row of this lane's segment, -1 for none (zeros).
+__device__ __forceinline__ void fetch_glu(const RowQuantArgs& a, const Place& at, int32_t row, int lane,
+                                          uint4 (*in)[32 * 4])
+{
+    const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
+    if (at.one) {
+        const int64_t base = row >= 0 ? ((int64_t)row * 2 * a.spr + (at.p - lane)) * 4 + lane : 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t h = glu_pair(gw[w], uw[w], gelu, a.act);
-            y[8 * k + 2 * w] = bf_lo(h);
-            y[8 * k + 2 * w + 1] = bf_hi(h);
+        for (int c = 0; c < 4; ++c) {
+            copy16(in[0] + slot_of(32 * c + lane), x4 + (row >= 0 ? base + 32 * c : 0), row >= 0);
+            copy16(in[1] + slot_of(32 * c + lane), x4 + (row >= 0 ? base + 32 * c + (int64_t)a.spr * 4 : 0),
+                   row >= 0);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int32_t r = __shfl_sync(0xFFFFFFFFu, row, 8 * c + lane / 4);
+            const uint32_t p = __shfl_sync(0xFFFFFFFFu, at.p, 8 * c + lane / 4);
+            const int64_t base = r >= 0 ? ((int64_t)r * 2 * a.spr + p) * 4 + lane % 4 : 0;
+            copy16(in[0] + slot_of(32 * c + lane), x4 + base, r >= 0);
+            copy16(in[1] + slot_of(32 * c + lane), x4 + (r >= 0 ? base + (int64_t)a.spr * 4 : 0), r >= 0);
         }
     }
 }
 
-template <int B, int ROT, int STRAT>
+// Walks a warp over its tiles of taken rows: the copies of the next tile are in flight, and
+// the row numbers of the one after it, while body(y, place, row) works on the current one.
+template <int ACT, class Body>
+__device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles, int lane,
+                                          uint4 (*in)[2][32 * 4], Body body)
+{
+    const int64_t step = (int64_t)gridDim.x * QTHREADS;
+    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
+    auto row_at = [&](const Place& at) { return at.live ? row_of(a, at.i, 0) : -1; };
+    Place now = place_of(a, s, lane);
+    int32_t row = row_at(now);
+    fetch_glu(a, now, row, lane, in[0]);
+    copies_commit();
+    bool more = blockIdx.x + (int64_t)gridDim.x < ntiles;
+    Place next = now;
+    int32_t next_row = -1;
+    if (more) {
+        next = place_of(a, s + step, lane);
+        next_row = row_at(next);
+    }
+    int buf = 0;
+    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1) {
+        Place then = next;
+        int32_t then_row = -1;
+        if (more)
+            fetch_glu(a, next, next_row, lane, in[buf ^ 1]);
+        copies_commit();
+        more = t + 2 * (int64_t)gridDim.x < ntiles;
+        if (more) {
+            then = place_of(a, s + 2 * step, lane);
+            then_row = row_at(then);
+        }
+        copies_wait_but_one();
+        __syncwarp();
+        if (s - lane < a.nseg) {  // warp-uniform
+            float y[SEG];
+            glu_segment<ACT>(in[buf][0], in[buf][1], lane, y);
+            body(y, now, row);
+        }
+        __syncwarp();
+        now = next;
+        row = next_row;
+        next = then;
+        next_row = then_row;
+    }
+}
+
+template <int B, int ROT, int STRAT, int ACT>
 __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     glu_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B> stage[QTHREADS / 32];
-    const int lane = threadIdx.x & 31;
-    WarpStage<B>& st = stage[threadIdx.x / 32];
-    QuantArgs qa = stage_args<B>(a, st);
+    __shared__ WarpStage<B, 2> stage[QTHREADS / 32];
     __shared__ float joined;
+    const int lane = threadIdx.x & 31;
+    WarpStage<B, 2>& st = stage[threadIdx.x / 32];
+    QuantArgs qa = stage_args(a, st.codes, st.scales);
     join_amax(a, joined, qa);
     build_scale_tables<STRAT>(tab, qa);
-    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += (int64_t)gridDim.x * QTHREADS) {
-        if (s - lane >= a.nseg)  // warp-uniform
-            break;
-        const bool live = s < a.nseg;
-        const uint32_t i = (uint32_t)s / a.spr;
-        const uint32_t p = (uint32_t)s - i * a.spr;
-        float y[SEG];
-        load_glu(a, live ? row_of(a, i, 0) : -1, p, y);
+    glu_tiles<ACT>(a, ntiles, lane, st.in, [&](float (&y)[SEG], const Place& at, int32_t row) {
         rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
         process_segment<B, STRAT, ROT>(y, lane, SEG, qa, tab);
         __syncwarp();
-        store_rows<B>(a, st, lane, i, p, live);
-        __syncwarp();
-    }
+        store_rows<B, STRAT>(a, st.codes, st.scales, tab, lane, at, [&](int) { return row; });
+    });
 }
 
 // Launch of a row quantize kernel over the resident CTAs, at most `most`.
@@ -341,5 +524,16 @@ cudaError_t launch_rows(K kernel, const RowQuantArgs& a, cudaStream_t st, int64_
     FP4Q_ROWS_CASE(KERNEL_, B_, S_, 32)  \
     FP4Q_ROWS_CASE(KERNEL_, B_, S_, 64)  \
     FP4Q_ROWS_CASE(KERNEL_, B_, S_, 128)
+#define FP4Q_GLU_CASE(B_, S_, R_)                                                        \
+    if (strat == S_ && rot == R_)                                                        \
+        return a.act == FP4Q_ACT_SILU                                                    \
+                   ? launch_rows(glu_quant_kernel<B_, R_, S_, FP4Q_ACT_SILU>, a, st)     \
+                   : launch_rows(glu_quant_kernel<B_, R_, S_, FP4Q_ACT_GELU_TANH>, a, st);
+#define FP4Q_GLU_ROTS(B_, S_)  \
+    FP4Q_GLU_CASE(B_, S_, 0)   \
+    FP4Q_GLU_CASE(B_, S_, 16)  \
+    FP4Q_GLU_CASE(B_, S_, 32)  \
+    FP4Q_GLU_CASE(B_, S_, 64)  \
+    FP4Q_GLU_CASE(B_, S_, 128)
 
 }  // namespace fp4q

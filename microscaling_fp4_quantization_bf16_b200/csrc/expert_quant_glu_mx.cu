@@ -4,8 +4,8 @@
 namespace fp4q {
 cudaError_t launch_glu_quant_mx(int strat, int rot, const RowQuantArgs& a, cudaStream_t st)
 {
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 32, K_MX)
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 32, K_MX_BRUTE)
+    FP4Q_GLU_ROTS(32, K_MX)
+    FP4Q_GLU_ROTS(32, K_MX_BRUTE)
     return cudaErrorInvalidValue;
 }
 }  // namespace fp4q

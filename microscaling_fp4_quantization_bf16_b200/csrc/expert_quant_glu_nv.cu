@@ -5,23 +5,26 @@ namespace fp4q {
 
 namespace {
 
-template <int ROT>
+template <int ROT, int ACT>
 __global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
     const int lane = threadIdx.x & 31;
+    __shared__ uint4 in[QTHREADS / 32][2][2][32 * 4];
     unsigned m = 0;
-    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += (int64_t)gridDim.x * QTHREADS) {
-        if (s - lane >= a.nseg)  // warp-uniform
-            break;
-        const uint32_t i = (uint32_t)s / a.spr;
-        float y[SEG];
-        load_glu(a, s < a.nseg ? row_of(a, i, 0) : -1, (uint32_t)s - i * a.spr, y);
+    glu_tiles<ACT>(a, ntiles, lane, in[threadIdx.x / 32], [&](float (&y)[SEG], const Place&, int32_t) {
         rotate_seg<ROT>(y, lane);
         m = max(m, seg_amax(y));
-    }
+    });
     put_amax(a, m);
+}
+
+template <int ROT>
+cudaError_t glu_amax_act(const RowQuantArgs& a, int* parts, cudaStream_t st)
+{
+    return a.act == FP4Q_ACT_SILU
+               ? launch_rows(glu_amax_kernel<ROT, FP4Q_ACT_SILU>, a, st, FP4Q_AMAX_WORK, parts)
+               : launch_rows(glu_amax_kernel<ROT, FP4Q_ACT_GELU_TANH>, a, st, FP4Q_AMAX_WORK, parts);
 }
 
 }  // namespace
@@ -29,21 +32,21 @@ __global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, int6
 cudaError_t launch_glu_amax(int rot, const RowQuantArgs& a, int* parts, cudaStream_t st)
 {
     switch (rot) {
-    case 0: return launch_rows(glu_amax_kernel<0>, a, st, FP4Q_AMAX_WORK, parts);
-    case 16: return launch_rows(glu_amax_kernel<16>, a, st, FP4Q_AMAX_WORK, parts);
-    case 32: return launch_rows(glu_amax_kernel<32>, a, st, FP4Q_AMAX_WORK, parts);
-    case 64: return launch_rows(glu_amax_kernel<64>, a, st, FP4Q_AMAX_WORK, parts);
-    case 128: return launch_rows(glu_amax_kernel<128>, a, st, FP4Q_AMAX_WORK, parts);
+    case 0: return glu_amax_act<0>(a, parts, st);
+    case 16: return glu_amax_act<16>(a, parts, st);
+    case 32: return glu_amax_act<32>(a, parts, st);
+    case 64: return glu_amax_act<64>(a, parts, st);
+    case 128: return glu_amax_act<128>(a, parts, st);
     default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_glu_quant_nv(int strat, int rot, const RowQuantArgs& a, cudaStream_t st)
 {
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_ABSMAX)
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_PREVENT_ZERO)
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_FOUR_OVER_SIX)
-    FP4Q_ROWS_ROTS(glu_quant_kernel, 16, K_BRUTE_FORCE)
+    FP4Q_GLU_ROTS(16, K_ABSMAX)
+    FP4Q_GLU_ROTS(16, K_PREVENT_ZERO)
+    FP4Q_GLU_ROTS(16, K_FOUR_OVER_SIX)
+    FP4Q_GLU_ROTS(16, K_BRUTE_FORCE)
     return cudaErrorInvalidValue;
 }
 }  // namespace fp4q
