@@ -50,16 +50,35 @@ struct Place {
     bool live, one;
 };
 
-__device__ __forceinline__ Place place_of(const RowQuantArgs& a, int64_t s, int lane)
-{
-    const uint32_t s0 = (uint32_t)(s - lane), i0 = s0 / a.spr, p0 = s0 - i0 * a.spr;
-    Place at{i0, p0 + lane, s < a.nseg, p0 + 32 <= a.spr};
-    while (at.p >= a.spr) {  // rows shorter than 32 segments: a warp spans several
-        at.p -= a.spr;
-        ++at.i;
+// The places of a warp's tiles, a grid's step apart: the division is done once,
+// a step adds its quotient and remainder.
+struct Places {
+    uint32_t i0, p0, di, dp;  // row and segment of the warp's first lane; the step
+
+    __device__ __forceinline__ Places(const RowQuantArgs& a, int64_t s0, int64_t step)
+        : i0((uint32_t)s0 / a.spr), p0((uint32_t)s0 - i0 * a.spr), di((uint32_t)step / a.spr),
+          dp((uint32_t)step - di * a.spr)
+    {
     }
-    return at;
-}
+    __device__ __forceinline__ void next(const RowQuantArgs& a)
+    {
+        i0 += di;
+        p0 += dp;
+        if (p0 >= a.spr) {
+            p0 -= a.spr;
+            ++i0;
+        }
+    }
+    __device__ __forceinline__ Place at(const RowQuantArgs& a, int lane, bool live) const
+    {
+        Place r{i0, p0 + lane, live, p0 + 32 <= a.spr};
+        while (r.p >= a.spr) {  // a warp that spans rows
+            r.p -= a.spr;
+            ++r.i;
+        }
+        return r;
+    }
+};
 
 // The destination row of choice j of token i; -1 where there is none.
 __device__ __forceinline__ int32_t row_of(const RowQuantArgs& a, int64_t i, int j)
@@ -230,10 +249,12 @@ __device__ __forceinline__ unsigned seg_amax(const float (&y)[SEG])
     return __float_as_uint(m);
 }
 
-// CTAs per SM that the registers are held to: searches as the compiler likes.
-template <int STRAT>
+// CTAs per SM that the registers are held to: searches as the compiler likes,
+// else 5 for tokens (6: 203 against 184 us for 16384 x 8192 to two experts each) and 4 behind the
+// activation (5 spills: 204 against 190 us for 8192 x 14336, MXFP4 H128).
+template <int STRAT, bool GLU>
 struct RowMinBlocks {
-    static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : 5;
+    static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : (GLU ? 4 : 5);
 };
 
 // ---------------------------------------------------------------- tokens
@@ -252,7 +273,7 @@ __device__ __forceinline__ void fetch_tokens(const RowQuantArgs& a, int64_t s0, 
 
 // Segment s of x is segment s % spr of token s / spr. Persistent CTAs.
 template <int B, int ROT, int STRAT>
-__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
+__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, false>::value)
     token_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
@@ -268,15 +289,16 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     copies_commit();
     join_amax(a, joined, qa);
     build_scale_tables<STRAT>(tab, qa);
+    Places places(a, s - lane, step);
     int buf = 0;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1) {
+    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1, places.next(a)) {
         if (t + gridDim.x < ntiles)
             fetch_tokens(a, s + step - lane, lane, st.in[buf ^ 1][0]);
         copies_commit();
         copies_wait_but_one();
         __syncwarp();
         if (s - lane < a.nseg) {  // warp-uniform
-            const Place at = place_of(a, s, lane);
+            const Place at = places.at(a, lane, s < a.nseg);
             // the rows of the first 32 choices, one a lane, on their way during the arithmetic
             int32_t mine = -1;
             if (at.one && lane < a.k)
@@ -302,39 +324,82 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 
 // ---------------------------------------------------------------- gated activation
 
-// h = bf16(fp32(g u sigmoid(z))) from its real value: 64 bits, one rounding to
-// fp32, one to bf16. Only pairs whose rounding the fp32 path cannot decide come here.
+// The fp32 evaluation of v = g u sigmoid(z) and the relative error E that bounds it.
+//
+// v = (g u) / (1 + 2^(-z log2 e)) with the hardware's 2^x and 1/x: 2^x is off by 2
+// units (2^-22) and its argument by 2^-23.4 |z| (product and constant), both times
+// the share t / (1 + t) of 2^x in the sum, which is small where z > 0;
+// the sum, the reciprocal (1 unit), two products and the ends of the bracket add
+// 6 half units, 2^-21.4; gelu's z itself is off by 2^-21.7 |z|. E = 2^-20.4 + c max(-z, 0)
+// with c = 2^-23 (silu) or 2^-21 (gelu) covers all of it. The ends v (1 -+ E) of the bracket round
+// to the same bf16 in all but about one value in three thousand.
 template <int ACT>
-static __device__ __noinline__ uint32_t glu_pair_exact(uint32_t g2, uint32_t u2)
+struct GluError {
+    static constexpr float base = 0x1.85p-21f;
+    static constexpr float slope = ACT == FP4Q_ACT_GELU_TANH ? 0x1p-21f : 0x1p-23f;
+};
+
+// g u sigmoid(z) in 64 bits by the library's functions, for what lies far out
+// (a call: hardly ever taken, so it holds no registers elsewhere).
+static __device__ __noinline__ double glu_far(double gu, double z) { return gu / (1.0 + exp(-z)); }
+
+// h = bf16(fp32(g u sigmoid(z))) from its real value: 64 bits, one rounding to
+// fp32, one to bf16. For values whose rounding the fp32 evaluation leaves open.
+// In its range (lim) e^-z = 2^n e^f, |f| <= ln 2 / 2, by e^f's Taylor polynomial of degree 13
+// (remainder below 2^-58), the quotient by Newton steps from the fp32
+// reciprocal: off by 2^-48 at most (the argument reduction at |z| = 60; 2^-51 near 0). Outside of
+// it by the library's exp and division.
+template <int ACT>
+__device__ __forceinline__ uint32_t glu_exact(float gf, float uf, bool lim)
 {
-    uint32_t out = 0;
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t gb = k ? g2 & 0xFFFF0000u : g2 << 16, ub = k ? u2 & 0xFFFF0000u : u2 << 16;
-        uint32_t h = (gb ^ ub) & 0x80000000u;  // a zero factor gives a signed zero
-        if (((gb << 1) != 0) && ((ub << 1) != 0)) {
-            const double g = (double)__uint_as_float(gb), u = (double)__uint_as_float(ub);
-            const double z = ACT == FP4Q_ACT_GELU_TANH
-                                 ? 1.5957691216057307612 * (g + 0.044715 * g * g * g)
-                                 : g;
-            h = __float_as_uint((float)(g * u / (1.0 + exp(-z))));
-        }
-        out |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(h))) << (16 * k);
+    const double g = (double)gf, u = (double)uf;
+    const double z = ACT == FP4Q_ACT_GELU_TANH ? 1.5957691216057307612 * (g + 0.044715 * g * g * g) : g;
+    double h;
+    if (lim && z < 600.0) {
+        const double n = rint(z * -1.4426950408889634074);
+        const double f = __fma_rn(n, -0.69314718055994530942, -z);
+        constexpr double c[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
+                                  1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600,
+                                  1.0 / 6227020800.0};
+        double e = c[13];
+#pragma unroll
+        for (int k = 12; k >= 0; --k)
+            e = __fma_rn(e, f, c[k]);
+        const double q = 1.0 + e * __longlong_as_double((long long)((int)n + 1023) << 52);
+        double r = (double)__frcp_rn((float)q);
+        r = __fma_rn(r, __fma_rn(-q, r, 1.0), r);
+        r = __fma_rn(r, __fma_rn(-q, r, 1.0), r);
+        h = g * u * r;
+    } else {
+        h = glu_far(g * u, z);
     }
-    return out;
+    return __bfloat16_as_ushort(__float2bfloat16_rn((float)h));
+}
+
+// One value of a pair again, alone: the fp32 evaluation if it decides, else 64 bits.
+template <int ACT>
+__device__ __forceinline__ uint32_t glu_one(uint32_t gb, uint32_t ub)
+{
+    if ((gb << 1) == 0 || (ub << 1) == 0)
+        return ((gb ^ ub) & 0x80000000u) >> 16;  // a zero factor gives a signed zero
+    const float g = __uint_as_float(gb), u = __uint_as_float(ub);
+    float z = g;
+    if constexpr (ACT == FP4Q_ACT_GELU_TANH)
+        z = (g * 1.5957691216f) * __fmaf_rn(g * 0.044715f, g, 1.0f);
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(z * -1.4426950409f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t + 1.0f));
+    const float v = (g * u) * r;
+    const float d = v * __fmaf_rn(fminf(z, 0.0f), -GluError<ACT>::slope, GluError<ACT>::base);
+    const bool lim = z > -60.0f && fabsf(v) > 0x1p-100f;
+    const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(v + d));
+    if (lim && __bfloat16_as_ushort(__float2bfloat16_rn(v - d)) == hi)
+        return hi;
+    return glu_exact<ACT>(g, u, lim);
 }
 
 // Two values of h as packed bf16, from packed bf16 gates and values, and whether
-// they are certain.
-//
-// v = (g u) / (1 + 2^(-z log2 e)) in fp32 with the hardware's 2^x and 1/x is
-// within E |v| of the real value: 2^x is off by 2^-22.5 and its argument
-// by 2^-23.4 |z| (products and constant), which count in full only where z < 0;
-// the sum, the reciprocal and two products add 2^-22 at most; gelu's z itself is off by 2^-22 |z|.
-// E = 2^-20 + 2^-21 max(-z, 0) covers all of it. The ends v (1 -+ E) of that
-// bracket round to the same bf16 in all but about one pair in a thousand; those, and
-// whatever leaves the range in which relative errors hold, are formed in 64 bits.
-// (Both halves of a pair run on packed fp32 operations.)
+// the fp32 evaluation decides both (packed operations).
 template <int ACT>
 __device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, bool& certain)
 {
@@ -352,10 +417,9 @@ __device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, bool& cer
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(t1));
     const f32x2 v = mul2(mul2(g, u), pk2(r0, r1));
     upk2(z, z0, z1);
-    const f32x2 err = fma2(pk2(fminf(z0, 0.0f), fminf(z1, 0.0f)), pk2(-0x1p-21f, -0x1p-21f),
-                           pk2(0x1p-20f, 0x1p-20f));
+    constexpr float base = GluError<ACT>::base, slope = -GluError<ACT>::slope;
+    const f32x2 d = mul2(v, fma2(pk2(fminf(z0, 0.0f), fminf(z1, 0.0f)), pk2(slope, slope), pk2(base, base)));
     float lo0, lo1, hi0, hi1, v0, v1;
-    const f32x2 d = mul2(v, err);
     upk2(add2(v, d), hi0, hi1);
     upk2(sub2(v, d), lo0, lo1);
     upk2(v, v0, v1);
@@ -391,7 +455,11 @@ __device__ __forceinline__ void glu_segment(uint4* gate, const uint4* value, int
         for (uint32_t m = redo; m != 0; m &= m - 1) {
             const int pair = __ffs(m) - 1;
             const int at = slot_of(4 * lane + pair / 4) * 4 + pair % 4;
-            gw[at] = glu_pair_exact<ACT>(gw[at], uw[at]);
+            uint32_t g2 = gw[at], u2 = uw[at], out = 0;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k, g2 >>= 16, u2 >>= 16)
+                out = (out >> 16) | (glu_one<ACT>(g2 << 16, u2 << 16) << 16);
+            gw[at] = out;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -412,12 +480,14 @@ __device__ __forceinline__ void fetch_glu(const RowQuantArgs& a, const Place& at
 {
     const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
     if (at.one) {
-        const int64_t base = row >= 0 ? ((int64_t)row * 2 * a.spr + (at.p - lane)) * 4 + lane : 0;
+        const bool real = row >= 0;
+        const uint4* g = x4 + (real ? ((int64_t)row * 2 * a.spr + (at.p - lane)) * 4 + lane : 0);
+        const uint4* u = g + (real ? (int64_t)a.spr * 4 : 0);
+        const int more = real ? 32 : 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            copy16(in[0] + slot_of(32 * c + lane), x4 + (row >= 0 ? base + 32 * c : 0), row >= 0);
-            copy16(in[1] + slot_of(32 * c + lane), x4 + (row >= 0 ? base + 32 * c + (int64_t)a.spr * 4 : 0),
-                   row >= 0);
+            copy16(in[0] + slot_of(32 * c + lane), g + c * more, real);
+            copy16(in[1] + slot_of(32 * c + lane), u + c * more, real);
         }
     } else {
 #pragma unroll
@@ -440,7 +510,8 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
     const int64_t step = (int64_t)gridDim.x * QTHREADS;
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     auto row_at = [&](const Place& at) { return at.live ? row_of(a, at.i, 0) : -1; };
-    Place now = place_of(a, s, lane);
+    Places places(a, s - lane, step);
+    Place now = places.at(a, lane, s < a.nseg);
     int32_t row = row_at(now);
     fetch_glu(a, now, row, lane, in[0]);
     copies_commit();
@@ -448,7 +519,8 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
     Place next = now;
     int32_t next_row = -1;
     if (more) {
-        next = place_of(a, s + step, lane);
+        places.next(a);
+        next = places.at(a, lane, s + step < a.nseg);
         next_row = row_at(next);
     }
     int buf = 0;
@@ -460,7 +532,8 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
         copies_commit();
         more = t + 2 * (int64_t)gridDim.x < ntiles;
         if (more) {
-            then = place_of(a, s + 2 * step, lane);
+            places.next(a);
+            then = places.at(a, lane, s + 2 * step < a.nseg);
             then_row = row_at(then);
         }
         copies_wait_but_one();
@@ -479,7 +552,7 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
 }
 
 template <int B, int ROT, int STRAT, int ACT>
-__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
+__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, true>::value)
     glu_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();

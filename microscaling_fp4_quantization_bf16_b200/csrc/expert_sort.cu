@@ -21,9 +21,9 @@ namespace fp4q {
 
 namespace {
 
-constexpr int STEPS = 8;               // 32-wide steps per warp, ids in registers
+constexpr int STEPS = 4;               // 32-wide steps per warp, ids in registers
 constexpr int MAXW = 32;               // warps of a block
-constexpr int SUB = MAXW * 32 * STEPS; // 8192 choices per pass of a block
+constexpr int SUB = MAXW * 32 * STEPS; // 4096 choices per pass of a block
 constexpr int MAX_BLOCKS = 148;
 
 template <class Id>
@@ -44,18 +44,23 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(SortArgs a)
         hist[e] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * a.chunk, hi = min(a.n, lo + a.chunk);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const int e = expert_of(static_cast<const Id*>(a.ids), i, hi, a.experts);
-        if (e >= 0)
-            atomicAdd(&hist[e], 1);
+    for (int64_t i0 = lo + threadIdx.x; i0 < hi; i0 += STEPS * blockDim.x) {
+        int e[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            e[s] = expert_of(static_cast<const Id*>(a.ids), i0 + s * blockDim.x, hi, a.experts);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            if (e[s] >= 0)
+                atomicAdd(&hist[e[s]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
         a.hist[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
-// Shared memory: rank counters [warps][experts], base [experts] (next free
-// row of each expert for this block).
+// Shared memory: rank counters [warps][experts], then per expert base (the next free
+// row for this block), its padded size and this pass's count.
 template <class Id>
 __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
 {
@@ -77,8 +82,8 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             e[s] = s < per_warp ? expert_of(static_cast<const Id*>(a.ids), run + 32 * s + lane, hi, E) : -1;
-        for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
-            cnt[i] = 0;
+        for (int i = threadIdx.x; i < (first ? warps + 2 : warps) * E; i += blockDim.x)
+            cnt[i] = 0;  // and base behind them
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
@@ -96,8 +101,26 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
             }
         }
         __syncthreads();
-        // counters -> exclusive over the warps; the block's total per expert
-        // goes to base on the first pass (to be turned into rows below)
+        // The counts of the blocks before this one and of all, once: a thread
+        // adds up every parts-th block of an expert, shared memory the parts
+        // (sums of whole numbers: the order does not matter).
+        if (first && !alone) {
+            const int parts = max(1, (int)blockDim.x / E);
+            for (int x = threadIdx.x; x < parts * E; x += blockDim.x) {
+                const int e1 = x % E;
+                int before = 0, total = 0;
+#pragma unroll 8
+                for (int b = x / E; b < (int)gridDim.x; b += parts) {
+                    const int c = a.hist[(int64_t)b * E + e1];
+                    before += b < (int)blockIdx.x ? c : 0;
+                    total += c;
+                }
+                atomicAdd(&base[e1], before);
+                atomicAdd(&base[E + e1], total);
+            }
+            __syncthreads();
+        }
+        // counters -> exclusive over the warps
         for (int x = threadIdx.x; x < E; x += blockDim.x) {
             int sum = 0;
             for (int w = 0; w < warps; ++w) {
@@ -106,16 +129,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
                 sum += c;
             }
             if (first) {
-                int before = 0, total = sum;
-                if (!alone) {
-                    total = 0;
-                    for (unsigned b = 0; b < gridDim.x; ++b) {
-                        const int c = a.hist[(int64_t)b * E + x];
-                        before += b < blockIdx.x ? c : 0;
-                        total += c;
-                    }
-                }
-                base[x] = before;
+                const int total = alone ? sum : base[E + x];
                 if (blockIdx.x == 0)
                     a.counts[x] = total;
                 // the padded size, for the scan over experts

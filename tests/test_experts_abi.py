@@ -75,9 +75,10 @@ def test_rows_limits(lib):
         assert lib.fp4q_expert_sort_work(n, e) == -1
         with pytest.raises(ValueError):
             fp4q.expert_rows(n, e)
-    assert lib.fp4q_expert_sort_work(8192, 64) == 0
-    assert lib.fp4q_expert_sort_work(8193, 64) == 2 * 64 * 4
-    assert lib.fp4q_expert_sort_work(10 ** 8, 64) == 148 * 64 * 4
+    # scratch: none while one block sorts, then a count per block and expert, at most 148 blocks
+    assert lib.fp4q_expert_sort_work(1024, 64) == 0
+    sizes = [lib.fp4q_expert_sort_work(n, 64) for n in (10 ** 4, 10 ** 5, 10 ** 6, 10 ** 8)]
+    assert sizes == sorted(sizes) and sizes[0] > 0 and sizes[-1] == 148 * 64 * 4
 
 
 def test_sort_validation(lib):

@@ -40,7 +40,7 @@ def untouched(t, rows_used):
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("tokens,k,experts,drop", [
     (1, 1, 1, 0), (1, 8, 64, 0), (33, 2, 8, 0.3), (0, 2, 8, 0), (64, 1, 1024, 0), (511, 8, 7, 0.1),
-    (1024, 8, 256, 0), (1025, 8, 256, 0.05), (3001, 5, 60, 0), (70000, 3, 128, 0.02),
+    (512, 8, 256, 0), (513, 8, 256, 0.05), (1024, 8, 256, 0), (1025, 8, 256, 0.05), (3001, 5, 60, 0), (70000, 3, 128, 0.02),
     (400000, 4, 1024, 0.01), (9000, 1, 1, 1.0)])
 def test_sort(gpu, dtype, tokens, k, experts, drop):
     ids = ref.route(tokens, k, experts, tokens + k, drop)
