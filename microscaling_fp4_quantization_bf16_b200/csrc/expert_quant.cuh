@@ -326,17 +326,19 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, false>::value)
 
 // The fp32 evaluation of v = g u sigmoid(z) and the relative error E that bounds it.
 //
-// v = (g u) / (1 + 2^(-z log2 e)) with the hardware's 2^x and 1/x: 2^x is off by 2
+// v = (g u) / (1 + 2^a), a = -z log2 e, with the hardware's 2^x and 1/x: 2^x is off by 2
 // units (2^-22) and its argument by 2^-23.4 |z| (product and constant), both times
-// the share t / (1 + t) of 2^x in the sum, which is small where z > 0;
+// the share of 2^a in the sum, which is small where z > 0;
 // the sum, the reciprocal (1 unit), two products and the ends of the bracket add
-// 6 half units, 2^-21.4; gelu's z itself is off by 2^-21.7 |z|. E = 2^-20.4 + c max(-z, 0)
-// with c = 2^-23 (silu) or 2^-21 (gelu) covers all of it. The ends v (1 -+ E) of the bracket round
+// 6 half units, 2^-21.4; gelu's z itself is off by 2^-21.7 |z|. With c = 2^-23 (silu) or
+// 2^-21 (gelu) for each unit of |z| and |z| <= (z^2 + 1) / 2, E = 2^-20.4 + c/2 + c/2 z^2
+// covers all of it (written in a^2 = z^2 log2(e)^2). The ends v (1 -+ E) of the bracket round
 // to the same bf16 in all but about one value in three thousand.
 template <int ACT>
 struct GluError {
-    static constexpr float base = 0x1.85p-21f;
-    static constexpr float slope = ACT == FP4Q_ACT_GELU_TANH ? 0x1p-21f : 0x1p-23f;
+    static constexpr float half = ACT == FP4Q_ACT_GELU_TANH ? 0x1p-22f : 0x1p-24f;
+    static constexpr float base = 0x1.85p-21f + half;
+    static constexpr float square = half * 0.4805f;  // 1 / log2(e)^2 = 0.48045...
 };
 
 // g u sigmoid(z) in 64 bits by the library's functions, for what lies far out
@@ -376,7 +378,11 @@ __device__ __forceinline__ uint32_t glu_exact(float gf, float uf, bool lim)
     return __bfloat16_as_ushort(__float2bfloat16_rn((float)h));
 }
 
-// One value of a pair again, alone: the fp32 evaluation if it decides, else 64 bits.
+// The range in which E holds: z > -60 keeps 2^a and its reciprocal in range,
+// |v| > 2^-100 the products (g u and v differ by a factor below 2^88).
+constexpr float GLU_Z = -60.0f, GLU_V = 0x1p-100f;
+
+// One value again, alone: the fp32 evaluation if it decides, else 64 bits.
 template <int ACT>
 __device__ __forceinline__ uint32_t glu_one(uint32_t gb, uint32_t ub)
 {
@@ -386,73 +392,79 @@ __device__ __forceinline__ uint32_t glu_one(uint32_t gb, uint32_t ub)
     float z = g;
     if constexpr (ACT == FP4Q_ACT_GELU_TANH)
         z = (g * 1.5957691216f) * __fmaf_rn(g * 0.044715f, g, 1.0f);
+    const float a = z * -1.4426950409f;
     float t, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(z * -1.4426950409f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(a));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t + 1.0f));
     const float v = (g * u) * r;
-    const float d = v * __fmaf_rn(fminf(z, 0.0f), -GluError<ACT>::slope, GluError<ACT>::base);
-    const bool lim = z > -60.0f && fabsf(v) > 0x1p-100f;
+    const float d = v * __fmaf_rn(a * a, GluError<ACT>::square, GluError<ACT>::base);
+    const bool lim = z > GLU_Z && fabsf(v) > GLU_V;
     const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(v + d));
     if (lim && __bfloat16_as_ushort(__float2bfloat16_rn(v - d)) == hi)
         return hi;
     return glu_exact<ACT>(g, u, lim);
 }
 
-// Two values of h as packed bf16, from packed bf16 gates and values, and whether
-// the fp32 evaluation decides both (packed operations).
-template <int ACT>
-__device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, bool& certain)
+// Two values of h as packed bf16, from packed bf16 gates and values (packed fp32
+// operations). Pair I's bit is set in open where the bracket's ends differ; zmin and
+// vmin collect the smallest z and |v|.
+template <int ACT, int I>
+__device__ __forceinline__ uint32_t glu_pair(uint32_t g2, uint32_t u2, uint32_t& open, float& zmin,
+                                             float& vmin)
 {
     const f32x2 g = pk2(bf_lo(g2), bf_hi<true>(g2)), u = pk2(bf_lo(u2), bf_hi<true>(u2));
     f32x2 z = g;
     if constexpr (ACT == FP4Q_ACT_GELU_TANH)
         z = mul2(mul2(g, pk2(1.5957691216f, 1.5957691216f)),
                  fma2(mul2(g, pk2(0.044715f, 0.044715f)), g, pk2(1.0f, 1.0f)));
+    const f32x2 a = mul2(z, pk2(-1.4426950409f, -1.4426950409f));
     float z0, z1, t0, t1, r0, r1;
-    upk2(mul2(z, pk2(-1.4426950409f, -1.4426950409f)), t0, t1);
+    upk2(a, t0, t1);
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
     upk2(add2(pk2(t0, t1), pk2(1.0f, 1.0f)), t0, t1);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(t0));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(t1));
     const f32x2 v = mul2(mul2(g, u), pk2(r0, r1));
-    upk2(z, z0, z1);
-    constexpr float base = GluError<ACT>::base, slope = -GluError<ACT>::slope;
-    const f32x2 d = mul2(v, fma2(pk2(fminf(z0, 0.0f), fminf(z1, 0.0f)), pk2(slope, slope), pk2(base, base)));
+    constexpr float base = GluError<ACT>::base, square = GluError<ACT>::square;
+    const f32x2 d = mul2(v, fma2(mul2(a, a), pk2(square, square), pk2(base, base)));
     float lo0, lo1, hi0, hi1, v0, v1;
     upk2(add2(v, d), hi0, hi1);
     upk2(sub2(v, d), lo0, lo1);
     upk2(v, v0, v1);
+    upk2(z, z0, z1);
+    zmin = fminf(fminf(zmin, z0), z1);
+    vmin = fminf(fminf(vmin, fabsf(v0)), fabsf(v1));
     const uint32_t hi = pack_bf16x2(hi0, hi1);
-    // z > -60 keeps 2^x and its reciprocal in range, |v| > 2^-100 the products
-    // (g u and v differ by a factor below 2^88); NaN fails too
-    certain = fminf(z0, z1) > -60.0f && fminf(fabsf(v0), fabsf(v1)) > 0x1p-100f &&
-              pack_bf16x2(lo0, lo1) == hi;
+    if (pack_bf16x2(lo0, lo1) != hi)
+        open |= 1u << I;
     return hi;
 }
 
 // This lane's segment of h, widened, from its gates and values in shared memory. The pairs
-// run without a branch between them; the uncertain ones follow one by one, patched through the gates' slots.
+// run without a branch between them; the undecided ones follow one by one, patched through
+// the gates' slots.
 template <int ACT>
 __device__ __forceinline__ void glu_segment(uint4* gate, const uint4* value, int lane, float (&y)[SEG])
 {
     uint4 h[4];
-    uint32_t redo = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    uint32_t open = 0;
+    float zmin = 0.0f, vmin = 1.0f;
+    static_for<4>([&](auto kc) {
+        constexpr int k = decltype(kc)::value;
         const uint4 g = gate[slot_of(4 * lane + k)], u = value[slot_of(4 * lane + k)];
-        bool c0, c1, c2, c3;
-        h[k].x = glu_pair<ACT>(g.x, u.x, c0);
-        h[k].y = glu_pair<ACT>(g.y, u.y, c1);
-        h[k].z = glu_pair<ACT>(g.z, u.z, c2);
-        h[k].w = glu_pair<ACT>(g.w, u.w, c3);
-        redo |= (c0 ? 0u : 1u << (4 * k)) | (c1 ? 0u : 2u << (4 * k)) | (c2 ? 0u : 4u << (4 * k)) |
-                (c3 ? 0u : 8u << (4 * k));
-    }
-    if (redo != 0) {
+        h[k].x = glu_pair<ACT, 4 * k>(g.x, u.x, open, zmin, vmin);
+        h[k].y = glu_pair<ACT, 4 * k + 1>(g.y, u.y, open, zmin, vmin);
+        h[k].z = glu_pair<ACT, 4 * k + 2>(g.z, u.z, open, zmin, vmin);
+        h[k].w = glu_pair<ACT, 4 * k + 3>(g.w, u.w, open, zmin, vmin);
+    });
+    // (an infinite v, as of an overflowing g u, has a bracket that ends in NaN: open)
+    if (!(zmin > GLU_Z && vmin > GLU_V))
+        open = 0xFFFFu;
+    if (open != 0) {
         uint32_t* gw = reinterpret_cast<uint32_t*>(gate);
         const uint32_t* uw = reinterpret_cast<const uint32_t*>(value);
-        for (uint32_t m = redo; m != 0; m &= m - 1) {
+        for (uint32_t m = open; m != 0; m &= m - 1) {
             const int pair = __ffs(m) - 1;
             const int at = slot_of(4 * lane + pair / 4) * 4 + pair % 4;
             uint32_t g2 = gw[at], u2 = uw[at], out = 0;
@@ -464,10 +476,10 @@ __device__ __forceinline__ void glu_segment(uint4* gate, const uint4* value, int
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const uint4 w = gate[slot_of(4 * lane + k)];
-            h[k].x = redo & (1u << (4 * k)) ? w.x : h[k].x;
-            h[k].y = redo & (2u << (4 * k)) ? w.y : h[k].y;
-            h[k].z = redo & (4u << (4 * k)) ? w.z : h[k].z;
-            h[k].w = redo & (8u << (4 * k)) ? w.w : h[k].w;
+            h[k].x = open & (1u << (4 * k)) ? w.x : h[k].x;
+            h[k].y = open & (2u << (4 * k)) ? w.y : h[k].y;
+            h[k].z = open & (4u << (4 * k)) ? w.z : h[k].z;
+            h[k].w = open & (8u << (4 * k)) ? w.w : h[k].w;
         }
     }
     unpack_seg<true>(h, y);
