@@ -26,8 +26,8 @@
  * least fp4q_expert_rows(T * k, experts), which covers every routing. Rows that hold no choice (the
  * end of a segment's last 128 rows, rows behind the last segment) are
  * neither read for a result nor written: they stay as they were. slots[t * k + j]
- * is the row of choice j of token t, or -1 for a choice that is dropped.
- * A choice may name the same expert twice; each gets a row.
+ * is the row of choice j of token t, or -1 for a choice that is dropped; no two
+ * choices share a row. A token may choose the same expert twice; each choice gets a row.
  */
 #ifndef FP4Q_EXPERTS_H
 #define FP4Q_EXPERTS_H
@@ -112,9 +112,9 @@ fp4q_status fp4q_expert_quantize(const void* x, int64_t tokens, int64_t cols, in
  *              w_global_scale float [experts] (NVFP4).
  * counts, starts  as written by fp4q_expert_sort. A segment that does not lie
  *              inside 0 .. rows or does not start at a multiple of 128 is left out.
- * mean_rows    the caller's estimate of the rows of an expert that has any
- *              (a speed hint: picks the tile; results do not depend on it
- *              beyond nothing at all -- every tile sums in the same order).
+ * mean_rows    the caller's estimate of the rows of an expert that has any: picks
+ *              the tile (one CTA or a pair), nothing else. Results of the two forms may
+ *              differ by the order of the fp32 sums.
  * d            [rows, N] of d_dtype; rows without a choice stay as they were.
  * K a multiple of 32, N of 4 (fp32 output) or 8 (bf16). Products accumulate
  * in fp32 on the tensor cores. rows == 0 enqueues nothing.

@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(GTHREADS, 1)
     }
     pdl_begin();
     if (warp == 0) {
-        // token tiles of the experts before each; segments outside the buffer count none
+        // Token tiles of the experts before each; segments outside the buffer
+        // count none, and all together no more than disjoint segments can have.
+        const int limit = (int)(p.rows / kSegRows);
         int carry = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
@@ -345,9 +347,10 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                 const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
                 inc += lane >= d ? v : 0;
             }
+            inc = min(carry + inc, limit);
             if (e < p.experts)
-                prefix[e + 1] = carry + inc;
-            carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+                prefix[e + 1] = inc;
+            carry = __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
         if (lane == 0)
             prefix[0] = 0;

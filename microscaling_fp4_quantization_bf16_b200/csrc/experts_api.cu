@@ -188,7 +188,7 @@ fp4q_status fp4q_expert_gemm(const uint8_t* a_codes, const uint8_t* a_mma_scales
     const bool out32 = d_dtype == FP4Q_OUT_F32;
     if (experts < 1 || experts > FP4Q_MAX_EXPERTS || rows < 0 || rows > kMaxRows ||
         rows % kSegRows != 0 || N <= 0 || K <= 0 || K % 32 != 0 || N % (out32 ? 4 : 8) != 0 ||
-        K > kMaxRows || N > kMaxRows || experts * N > kMaxRows || mean_rows < 0)
+        K > kMaxRows || N > kMaxRows || experts * N > kMaxRows - 1024 || mean_rows < 0)
         return FP4Q_ERR_SHAPE;
     if (rows == 0)
         return FP4Q_OK;

@@ -129,7 +129,8 @@ def test_quantize_rows(gpu, fmt, strategy, rot):
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("tokens,k,experts,cols,dq", [
     (1, 1, 1, 32, torch.float32), (1, 8, 64, 1056, torch.bfloat16), (5, 2, 3, 96, torch.float32),
-    (300, 1, 4, 160, None), (129, 64, 1024, 64, torch.bfloat16), (1000, 2, 2, 4064, torch.float32)])
+    (300, 1, 4, 160, None), (129, 64, 1024, 64, torch.bfloat16), (1000, 2, 2, 4064, torch.float32),
+    (7, 40, 64, 2048, torch.bfloat16)])
 def test_quantize_shapes(gpu, fmt, tokens, k, experts, cols, dq):
     x = synth.laplace_outliers(tokens, cols, seed=cols)
     ids = ref.route(tokens, k, experts, cols, 0.02)
@@ -303,6 +304,20 @@ def test_product_equals_the_dense_product(gpu):
     assert (np.abs(ref.to64(d[:M]) - ref.to64(dense)) <= bound).all()
 
 
+def test_product_forms_agree(gpu):
+    """One CTA or a pair to a tile, on the same operands (through the C call's mean_rows): both within the fp32 bound."""
+    experts, N, K = 5, 392, 608
+    p, q, w = operands(gpu, ref.route(900, 2, experts, 4, 0.05), experts, N, K, "nvfp4", 4)
+    for mean in (1, 128, 129, 10 ** 6):
+        d = filled((p.rows, N), torch.float32)
+        st = gpu.load().fp4q_expert_gemm(q.codes.data_ptr(), q.scales.data_ptr(), q.global_scale.data_ptr(),
+                                         w.codes.data_ptr(), w.scales.data_ptr(), w.global_scale.data_ptr(),
+                                         p.counts.data_ptr(), p.starts.data_ptr(), experts, p.rows, N, K, 0, mean,
+                                         d.data_ptr(), 0, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        assert untouched(d, check_product(p, q, w, d, "nvfp4", N, K, True))
+
+
 def test_product_leaves_out_bad_segments(gpu):
     """Segments that do not fit the buffer or start off a row tile are not computed."""
     experts, N, K = 4, 64, 128
@@ -471,6 +486,126 @@ def test_dispatch_gradient(gpu):
     # dx is off by (k + log2 rot + 2) half steps of a chunk's terms, and dy was rounded to fp32 once
     noise = (k + 6 + 4) * U24 * np.abs(x).max() * np.abs(dy).sum() * np.sqrt(rot)
     assert abs(lhs - rhs) <= noise
+
+
+# ---------------------------------------------------------------- more than 2^31 elements
+
+def big_plan(gpu, tokens, experts=2):
+    ids = torch.randint(0, experts, (tokens, 1), generator=torch.Generator().manual_seed(1)).cuda()
+    p = gpu.expert_sort(ids, experts)
+    slots = p.slots.reshape(-1)
+    last = torch.cat([slots.topk(4).indices, slots.topk(3, largest=False).indices, torch.tensor([tokens // 2]).cuda()])
+    return p, last, slots[last].long()
+
+
+def patterned(rows, cols):
+    """bf16 [rows, cols] whose rows repeat every 257."""
+    base = synth.gaussian(257, cols, seed=3).cuda()
+    return base.repeat(-(-rows // 257), 1)[:rows].contiguous()
+
+
+def test_combine_beyond_32_bits(gpu):
+    tokens, cols = 270000, 8192
+    p, t, r = big_plan(gpu, tokens)
+    y = patterned(p.rows, cols)
+    assert y.numel() > 2 ** 31 and int(r.max()) * cols > 2 ** 31
+    w = torch.full((tokens, 1), 0.5, device="cuda")
+    out = gpu.expert_combine(y, p, w)
+    assert torch.equal(out[t], (y[r].float() * 0.5).to(torch.bfloat16))     # exact: a power of two
+    dy, dw = gpu.expert_combine_bwd(out, y, p, w, out=y.clone())
+    assert torch.equal(dy[r], (out[t].float() * 0.5).to(torch.bfloat16))
+    want = (out[t].double() * y[r].double()).sum(1)
+    assert ((dw[t, 0].double() - want).abs() <= cols * U24 * (out[t].double() * y[r].double()).abs().sum(1)).all()
+
+
+def test_quantizers_beyond_32_bits(gpu):
+    tokens, cols = 270000, 8192
+    p, t, r = big_plan(gpu, tokens)
+    x = patterned(tokens, cols)
+    q = gpu.expert_quantize(x, p, "mxfp4", "absmax", 32)
+    want = ref.quantize(ref.bits(x[t]), "mxfp4", "absmax", 32)
+    assert np.array_equal(q.codes[r].cpu().numpy(), want["codes"])
+    del x
+    gu = patterned(p.rows, 2 * cols)
+    q = gpu.glu_quantize(gu, "mxfp4", "absmax", 0, p, out=q)
+    want = ref.quantize(ref.glu(ref.bits(gu[r]), "silu"), "mxfp4", "absmax", 0)
+    assert np.array_equal(q.codes[r].cpu().numpy(), want["codes"])
+    sc = ref.mma_rows(q.scales.cpu().numpy(), p.rows, cols // 32)
+    assert np.array_equal(sc[r.cpu().numpy()], want["scales"])
+    dh = patterned(p.rows, cols)
+    out = gpu.glu_bwd(gu, dh, p)
+    few = gpu.glu_bwd(gu[r].contiguous(), dh[r].contiguous())
+    assert torch.equal(out[r], few)
+
+
+def test_product_beyond_32_bits(gpu):
+    tokens, N, K = 140000, 16384, 64
+    p, t, r = big_plan(gpu, tokens)
+    q = gpu.expert_quantize(patterned(tokens, K), p, "mxfp4")
+    w = gpu.expert_weights(patterned(2 * N, K).reshape(2, N, K), "mxfp4")
+    d = gpu.expert_gemm(q.codes, q.scales, None, w.codes, w.scales, None, p, "mxfp4")
+    assert int(r.max()) * N > 2 ** 31
+    starts = p.starts.tolist()
+    a = ref.values(q.codes.cpu().numpy(), q.scales.cpu().numpy(), p.rows, K, "mxfp4")
+    for row in r.tolist():
+        e = 0 if row < starts[1] else 1
+        b = ref.values(w.codes[e].cpu().numpy(), w.scales[e].cpu().numpy(), N, K, "mxfp4")
+        want = b @ a[row]
+        bound = (K + 1) * U24 * (np.abs(b) @ np.abs(a[row]))
+        assert (np.abs(ref.to64(d[row]) - want) <= bound + UBF * (np.abs(want) + bound)).all()
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_refusals(gpu):
+    """Arguments that do not belong together raise before anything runs."""
+    p = plan_of(gpu, ref.route(20, 2, 4, 1), 4)
+    x = torch.zeros(20, 64, dtype=torch.bfloat16, device="cuda")
+    q = gpu.expert_quantize(x, p, "mxfp4")
+    w = gpu.expert_weights(torch.zeros(4, 32, 64, dtype=torch.bfloat16, device="cuda"), "mxfp4")
+    y = torch.zeros(p.rows, 64, dtype=torch.bfloat16, device="cuda")
+    wt = torch.zeros(20, 2, device="cuda")
+    mm = lambda **k: gpu.expert_gemm(k.get("a", q.codes), k.get("sa", q.scales), None, k.get("w", w.codes),  # noqa: E731
+                                     k.get("sw", w.scales), None, k.get("p", p), "mxfp4", out=k.get("out"))
+    bad = [
+        lambda: gpu.expert_sort(torch.zeros(4, 2, dtype=torch.int16, device="cuda"), 4),
+        lambda: gpu.expert_sort(torch.zeros(4, dtype=torch.int32, device="cuda"), 4),
+        lambda: gpu.expert_sort(torch.zeros(2, 4, dtype=torch.int32, device="cuda").t(), 4),
+        lambda: gpu.expert_sort(torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 0),
+        lambda: gpu.expert_sort(torch.zeros(200, 2, dtype=torch.int32, device="cuda"), 4, rows=128),
+        lambda: gpu.expert_sort(torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 4, rows=1000),
+        lambda: gpu.expert_quantize(x.float(), p),
+        lambda: gpu.expert_quantize(x[:19], p),
+        lambda: gpu.expert_quantize(x[:, :48].contiguous(), p),
+        lambda: gpu.expert_quantize(x, p, "ue5m3"),
+        lambda: gpu.expert_quantize(x, p, "mxfp4", "four_over_six"),
+        lambda: gpu.expert_quantize(x, p, "nvfp4", rot=128),
+        lambda: gpu.expert_quantize(x, p, "nvfp4", global_amax=torch.zeros(2, device="cuda")),
+        lambda: gpu.expert_quantize(x, p, "mxfp4", out=gpu.Quantized(q.codes[:128], q.scales, None, None, None)),
+        lambda: mm(a=q.codes[:, :16].contiguous()),
+        lambda: mm(sa=q.scales[:-1]),
+        lambda: mm(w=w.codes[:3]),
+        lambda: mm(sw=w.scales[:, :512].contiguous()[:2]),
+        lambda: mm(out=torch.zeros(p.rows, 40, dtype=torch.bfloat16, device="cuda")),
+        lambda: mm(out=torch.zeros(p.rows, 32, dtype=torch.float16, device="cuda")),
+        lambda: gpu.expert_gemm(q.codes, q.scales, None, w.codes, w.scales, None, p, "nvfp4"),
+        lambda: gpu.expert_weights(torch.zeros(4, 32, 40, dtype=torch.bfloat16, device="cuda")),
+        lambda: gpu.glu_quantize(y[:, :63].contiguous()),
+        lambda: gpu.glu_quantize(y[:100], plan=p),
+        lambda: gpu.glu_quantize(y, act="relu"),
+        lambda: gpu.glu_bwd(y, y, p),
+        lambda: gpu.expert_combine(y[:128], p),
+        lambda: gpu.expert_combine(y, p, wt[:, :1].contiguous()),
+        lambda: gpu.expert_combine(y, p, wt.double()),
+        lambda: gpu.expert_combine(y, p, rot=48),
+        lambda: gpu.expert_combine_bwd(x[:, :32].contiguous(), y, p),
+        lambda: gpu.expert_combine_bwd(x, y, p, out=torch.zeros_like(y, dtype=torch.float32)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, gpu.Fp4qError)):
+            call()
+            raise AssertionError(f"call {i} was accepted")
+    torch.cuda.synchronize()
 
 
 # ---------------------------------------------------------------- a whole layer
