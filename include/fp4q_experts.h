@@ -75,15 +75,18 @@ fp4q_status fp4q_expert_sort(const void* ids, int id_bytes, int64_t n, int64_t e
 
 /*
  * fp4q_expert_quantize -- fp4q_quantize_mma of every token, written to the
- * rows of its choices: bit for bit the codes and scale bytes that quantizing
- * the gathered rows would give. A token is quantized once.
+ * rows of its choices: for a given abs-max (and for MXFP4) bit for bit the codes and scale
+ * bytes that quantizing the gathered rows gives. A token is quantized once.
  * x            bf16 [tokens, cols]; cols a multiple of 32 and of rot.
  * slots        int32 [tokens, k]; a value outside 0 .. rows-1 is skipped.
  * rows         rows of the outputs, a multiple of 128.
  * fmt, strat, rot as fp4q_quantize_mma (NVFP4 block 16, MXFP4 block 32).
- * global_amax_in   NVFP4: device float with a calibrated abs-max, or NULL to
+ * global_amax_in   NVFP4: device float with a calibrated abs-max (s_g = amax /
+ *              2688, one division, as fp4q_quantize), or NULL to
  *              take the abs-max of all of x (rotated; tokens without a choice
- *              included) in an extra pass. Ignored for MXFP4.
+ *              included) in an extra pass; s_g is then that maximum times fp32(1 / 2688), which
+ *              may be one unit in the last place from the quotient (for
+ *              fp4q_quantize's own bits pass fp4q_global_amax's value). Ignored for MXFP4.
  * global_scale_out NVFP4: device float, receives s_g.
  * amax_work    FP4Q_AMAX_WORK device floats of scratch, needed when fmt is NVFP4 and
  *              global_amax_in is NULL; distinct from global_scale_out.
@@ -138,7 +141,7 @@ fp4q_status fp4q_expert_gemm(const uint8_t* a_codes, const uint8_t* a_mma_scales
  *              NULL for all rows (n is ignored).
  * cols         a multiple of 32 and of rot; other arguments as
  *              fp4q_expert_quantize. global_amax_in NULL (NVFP4) takes the
- *              abs-max of the rotated h over the rows taken. Without slots,
+ *              abs-max of the rotated h over the rows taken, and s_g from it as there. Without slots,
  *              rows may be any number and mma_scales has
  *              fp4q_mma_scale_bytes(rows, cols, fmt) bytes.
  * Inputs and a(g) * u must be finite.

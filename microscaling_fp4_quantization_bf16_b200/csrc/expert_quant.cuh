@@ -186,8 +186,8 @@ __device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, uint4* co
     QuantArgs q;
     q.x = nullptr;
     q.n = 0;
-    q.amax = a.amax;
-    q.sg_out = a.sg_out;
+    q.amax = nullptr;
+    q.sg_out = nullptr;
     q.codes = reinterpret_cast<uint8_t*>(codes);
     q.scales = scales;
     q.mse = nullptr;
@@ -199,29 +199,45 @@ __device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, uint4* co
     return q;
 }
 
-// The tensor abs-max that build_scale_tables reads, from the maxima of the
-// abs-max pass's CTAs (every CTA takes their maximum itself: no launch
-// in between, no value to clear beforehand). Ends with a CTA barrier.
-__device__ __forceinline__ void join_amax(const RowQuantArgs& a, float& joined, QuantArgs& q)
+// The NVFP4 tables of a CTA (see ScaleTables), from the calibrated abs-max, or
+// from the maxima of the abs-max pass's CTAs: every CTA joins them itself
+// (no launch in between, no value to clear beforehand), and takes s_g as their maximum times
+// 1 / 2688, one product, where a calibrated abs-max is divided. CTA 0 publishes s_g. Ends
+// with a CTA barrier.
+template <int STRAT>
+__device__ __forceinline__ void row_scale_tables(const RowQuantArgs& a, ScaleTables<STRAT>& tab)
 {
-    if (a.amax_parts == 0)  // uniform
-        return;
-    __shared__ unsigned top[QTHREADS / 32];
-    unsigned m = 0;
-    for (int i = threadIdx.x; i < a.amax_parts; i += QTHREADS)
-        m = max(m, __float_as_uint(a.amax[i]));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (threadIdx.x % 32 == 0)
-        top[threadIdx.x / 32] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if constexpr (!is_mx_strat(STRAT)) {
+        static_assert(QTHREADS == 128, "one table entry a thread");
+        __shared__ unsigned top[QTHREADS / 32];
+        float sg;
+        if (a.amax_parts == 0) {
+            sg = global_scale_of(*a.amax);
+        } else {
+            unsigned m = 0;
+            for (int i = threadIdx.x; i < a.amax_parts; i += QTHREADS)
+                m = max(m, __float_as_uint(a.amax[i]));
+            m = __reduce_max_sync(0xFFFFFFFFu, m);
+            if (threadIdx.x % 32 == 0)
+                top[threadIdx.x / 32] = m;
+            __syncthreads();
 #pragma unroll
-        for (int w = 1; w < QTHREADS / 32; ++w)
-            m = max(m, top[w]);
-        joined = __uint_as_float(m);
+            for (int w = 0; w < QTHREADS / 32; ++w)
+                m = max(m, top[w]);
+            sg = __fmul_rn(__uint_as_float(m), 1.0f / 2688.0f);
+            sg = sg > 0.0f && sg <= FLT_MAX ? sg : 1.0f;
+        }
+        const int c = threadIdx.x;
+        const float S = c <= 0x7E ? __fmul_rn(e4m3_dec((uint32_t)c), sg) : 0.0f;
+        tab.S[c] = S;
+        tab.R[c] = S == 0.0f ? 0.0f : guarded_rcp(S);
+        if (c == 0) {
+            tab.k = nv_consts(sg);
+            if (blockIdx.x == 0)
+                *a.sg_out = sg;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    q.amax = &joined;
 }
 
 // Writes the CTA's maximum of m (bits of non-negative floats).
@@ -279,16 +295,14 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, false>::value)
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
     __shared__ WarpStage<B, 1> stage[QTHREADS / 32];
-    __shared__ float joined;
     const int lane = threadIdx.x & 31;
     WarpStage<B, 1>& st = stage[threadIdx.x / 32];
-    QuantArgs qa = stage_args(a, st.codes, st.scales);
+    const QuantArgs qa = stage_args(a, st.codes, st.scales);
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * QTHREADS;
     fetch_tokens(a, s - lane, lane, st.in[0][0]);
     copies_commit();
-    join_amax(a, joined, qa);
-    build_scale_tables<STRAT>(tab, qa);
+    row_scale_tables<STRAT>(a, tab);
     Places places(a, s - lane, step);
     int buf = 0;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1, places.next(a)) {
@@ -570,12 +584,10 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, true>::value)
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
     __shared__ WarpStage<B, 2> stage[QTHREADS / 32];
-    __shared__ float joined;
     const int lane = threadIdx.x & 31;
     WarpStage<B, 2>& st = stage[threadIdx.x / 32];
-    QuantArgs qa = stage_args(a, st.codes, st.scales);
-    join_amax(a, joined, qa);
-    build_scale_tables<STRAT>(tab, qa);
+    const QuantArgs qa = stage_args(a, st.codes, st.scales);
+    row_scale_tables<STRAT>(a, tab);
     glu_tiles<ACT>(a, ntiles, lane, st.in, [&](float (&y)[SEG], const Place& at, int32_t row) {
         rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
         process_segment<B, STRAT, ROT>(y, lane, SEG, qa, tab);

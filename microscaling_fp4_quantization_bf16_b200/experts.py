@@ -216,7 +216,8 @@ def expert_quantize(x: torch.Tensor, plan: ExpertPlan, fmt="nvfp4", strategy="ab
     """quantize_mma() of bf16 tokens [tokens, cols] into the rows of their
     choices; each token is quantized once. Returns a Quantized of
     [plan.rows, cols] with MMA-layout scales (and dequantized values in
-    .dq, if dq_dtype or out.dq asks for them)."""
+    .dq, if dq_dtype or out.dq asks for them). NVFP4 without global_amax takes the
+    abs-max of x in an extra pass (see fp4q_expert_quantize for its s_g)."""
     tokens, cols = _matrix(x, "x", torch.bfloat16)
     dev = x.device
     _plan_args(plan, dev)

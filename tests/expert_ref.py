@@ -27,10 +27,77 @@ def bits(t):
     return t.view(torch.int16).cpu().numpy().view(np.uint16)
 
 
+F = np.float32
+
+
+def _rotate32(y, rot):
+    """Butterflies of ascending distance in fp32, then one factor: the definition's rotation."""
+    h = 1
+    shape = y.shape
+    while h < rot:
+        p = y.reshape(-1, 2, h)
+        y = np.stack([p[:, 0] + p[:, 1], p[:, 0] - p[:, 1]], 1)
+        h *= 2
+    return y.reshape(shape) * F(1 / math.sqrt(rot)) if rot else y.reshape(shape)
+
+
+def _tree(v):
+    while v.shape[-1] > 1:
+        v = v[..., 0::2] + v[..., 1::2]
+    return v[..., 0]
+
+
+def _nvfp4(y, strategy, sg):
+    """Codes, scale bytes and values of fp32 y [rows, cols] under s_g, one fp32 operation a step (the oracle's
+    steps, which takes an abs-max only)."""
+    v = y.reshape(y.shape[0], -1, 16)
+    top = np.abs(v).max(-1, keepdims=True)
+    e4m3 = np.array([oracle.e4m3_value(c) for c in range(0x7F)])
+    mid = (e4m3[1:] + e4m3[:-1]) / 2
+
+    def candidate(byte):
+        S = e4m3.astype(F)[byte] * sg
+        with np.errstate(divide="ignore"):
+            r = np.where(S == 0, F(0), np.minimum(F(1) / S, np.finfo(F).max))
+        a = np.abs(v * r).astype(np.float64)
+        steps = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0])
+        m = sum((a >= t) if i % 2 else (a > t) for i, t in enumerate(steps))
+        code = np.where(S == 0, 0, m + 8 * np.signbit(v))
+        w = E2M1.astype(F)[code] * S
+        d = v - w
+        return byte, code, w, _tree(d * d)[..., None]
+
+    def nearest(target):
+        x = (top / (sg * F(target))).astype(np.float64)
+        k = np.searchsorted(mid, x, side="left")            # ties: below, then up to the even code
+        tie = (k < 126) & (np.append(mid, np.inf)[np.minimum(k, 126)] == x) & (k % 2 == 1)
+        return np.minimum(k + tie, 0x7E)
+    best = candidate(nearest(6))
+    if strategy == "prevent_zero":
+        best = candidate(np.maximum(best[0], 1))
+    elif strategy == "four_over_six":
+        other = candidate(nearest(4))
+        take = other[3] < best[3]
+        best = [np.where(take, o, b) for o, b in zip(other, best)]
+    elif strategy == "brute_force":
+        best = candidate(np.full_like(best[0], 1))
+        for c in range(2, 0x7F):
+            other = candidate(np.full_like(best[0], c))
+            take = other[3] < best[3]
+            best = [np.where(take, o, b) for o, b in zip(other, best)]
+    byte, code, w, _ = best
+    code = code.reshape(y.shape).astype(np.uint8)
+    return {"codes": code[:, 0::2] | (code[:, 1::2] << 4), "scales": byte[..., 0].astype(np.uint8),
+            "global_scale": sg, "dq": w.reshape(y.shape).astype(F)}
+
+
 def quantize(x_bits, fmt, strategy, rot, amax=None):
-    """Oracle codes, row-major scales, values (fp32) and s_g of bf16 bit patterns."""
-    return oracle.quantize(x_bits, fmt, BLOCK[fmt], strategy, rot, dq="f32",
-                           **({} if amax is None else {"global_amax": amax}))
+    """Codes, row-major scales, values (fp32) and s_g of bf16 bit patterns: the oracle's for a given abs-max and for
+    MXFP4; for NVFP4 without one the same steps under s_g = abs-max * fp32(1 / 2688)."""
+    if fmt == "mxfp4" or amax is not None:
+        return oracle.quantize(x_bits, fmt, BLOCK[fmt], strategy, rot, dq="f32", global_amax=amax)
+    y = _rotate32((x_bits.astype(np.uint32) << 16).view(F), rot)
+    return _nvfp4(y, strategy, np.abs(y).max() * F(1 / 2688))
 
 
 def mma_rows(flat, rows, blocks):

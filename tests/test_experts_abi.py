@@ -265,3 +265,19 @@ def test_scale_bytes_agree(lib):
     for fmt, f in (("nvfp4", NV), ("mxfp4", MX)):
         for rows, cols in ((1, 32), (128, 64), (300, 1056), (5, 4096)):
             assert experts.scale_bytes(rows, cols, fmt) == lib.fp4q_mma_scale_bytes(rows, cols, f)
+
+
+@pytest.mark.parametrize("strategy", ["absmax", "prevent_zero", "four_over_six", "brute_force"])
+@pytest.mark.parametrize("rot", [0, 16, 128])
+def test_reference_steps_are_the_oracles(strategy, rot):
+    """The fp32 steps that the GPU tests hold NVFP4 without a given abs-max to, against the oracle under its s_g."""
+    rng = np.random.default_rng(rot)
+    x = torch.from_numpy(rng.laplace(0, 1, (24, 256)) * (1 + 20 * (rng.random((24, 256)) < 0.01))).to(torch.bfloat16)
+    x[3, :64] = 0
+    x[4] *= 2.0 ** -40
+    bits = ref.bits(x)
+    want = ref.quantize(bits, "nvfp4", strategy, rot, 77.0)
+    y = ref._rotate32((bits.astype(np.uint32) << 16).view(np.float32), rot)
+    got = ref._nvfp4(y, strategy, np.float32(77.0) / np.float32(2688))
+    for k in ("codes", "scales", "dq"):
+        assert np.array_equal(got[k], want[k]), k
