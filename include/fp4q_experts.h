@@ -18,6 +18,12 @@
  * integers (ids, counts, starts, slots) cannot be checked on the host; what
  * the kernels do with bad ones is said at each entry point.
  *
+ * State beyond fp4q.h's list: the resident CTAs per SM of each row quantize
+ * kernel, and one bit per product kernel and device (its shared-memory limit
+ * has been raised). The product's waits are bounded like the TMA-fed
+ * quantizer's; one that runs out ends the call early and adds to the counter of
+ * fp4q_device_errors.
+ *
  * The row layout. The choices of T tokens, k each, are spread over
  * `experts` segments of rows: expert e's rows are starts[e] ..
  * starts[e] + counts[e] - 1, in the order of the choices, and every start is a
