@@ -596,25 +596,44 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, true>::value)
     });
 }
 
+// Resident CTAs per SM of one kernel (a template value, so that each kernel
+// keeps its own), queried once per process, times the SMs of the current device.
+template <auto KERNEL>
+int64_t resident_rows()
+{
+    static std::atomic<int> per_sm{0};
+    int dev = 0, sms = 0, n = per_sm.load(std::memory_order_relaxed);
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return -1;
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, QTHREADS, 0) != cudaSuccess)
+            return -1;
+        n = n < 1 ? 1 : n;
+        per_sm.store(n, std::memory_order_relaxed);
+    }
+    return (int64_t)sms * n;
+}
+
 // Launch of a row quantize kernel over the resident CTAs, at most `most`.
-template <class K>
-cudaError_t launch_rows(K kernel, const RowQuantArgs& a, cudaStream_t st, int64_t most = 0x7FFFFFFF,
+template <auto KERNEL>
+cudaError_t launch_rows(const RowQuantArgs& a, cudaStream_t st, int64_t most = 0x7FFFFFFF,
                         int* ctas = nullptr)
 {
     const int64_t nblk = (a.nseg + QTHREADS - 1) / QTHREADS;
-    const int64_t res = resident_ctas(kernel);
+    const int64_t res = resident_rows<KERNEL>();
     if (res < 0)
         return cudaErrorUnknown;
     int64_t grid = nblk < res ? nblk : res;
     grid = grid < most ? grid : most;
     if (ctas != nullptr)
         *ctas = (int)grid;
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(QTHREADS), 0, st, a, nblk);
+    return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(QTHREADS), 0, st, a, nblk);
 }
 
 #define FP4Q_ROWS_CASE(KERNEL_, B_, S_, R_) \
     if (strat == S_ && rot == R_)           \
-        return launch_rows(KERNEL_<B_, R_, S_>, a, st);
+        return launch_rows<KERNEL_<B_, R_, S_>>(a, st);
 #define FP4Q_ROWS_ROTS(KERNEL_, B_, S_)  \
     FP4Q_ROWS_CASE(KERNEL_, B_, S_, 0)   \
     FP4Q_ROWS_CASE(KERNEL_, B_, S_, 16)  \
@@ -624,8 +643,8 @@ cudaError_t launch_rows(K kernel, const RowQuantArgs& a, cudaStream_t st, int64_
 #define FP4Q_GLU_CASE(B_, S_, R_)                                                        \
     if (strat == S_ && rot == R_)                                                        \
         return a.act == FP4Q_ACT_SILU                                                    \
-                   ? launch_rows(glu_quant_kernel<B_, R_, S_, FP4Q_ACT_SILU>, a, st)     \
-                   : launch_rows(glu_quant_kernel<B_, R_, S_, FP4Q_ACT_GELU_TANH>, a, st);
+                   ? launch_rows<glu_quant_kernel<B_, R_, S_, FP4Q_ACT_SILU>>(a, st)     \
+                   : launch_rows<glu_quant_kernel<B_, R_, S_, FP4Q_ACT_GELU_TANH>>(a, st);
 #define FP4Q_GLU_ROTS(B_, S_)  \
     FP4Q_GLU_CASE(B_, S_, 0)   \
     FP4Q_GLU_CASE(B_, S_, 16)  \

@@ -23,8 +23,8 @@ template <int ROT>
 cudaError_t glu_amax_act(const RowQuantArgs& a, int* parts, cudaStream_t st)
 {
     return a.act == FP4Q_ACT_SILU
-               ? launch_rows(glu_amax_kernel<ROT, FP4Q_ACT_SILU>, a, st, FP4Q_AMAX_WORK, parts)
-               : launch_rows(glu_amax_kernel<ROT, FP4Q_ACT_GELU_TANH>, a, st, FP4Q_AMAX_WORK, parts);
+               ? launch_rows<glu_amax_kernel<ROT, FP4Q_ACT_SILU>>(a, st, FP4Q_AMAX_WORK, parts)
+               : launch_rows<glu_amax_kernel<ROT, FP4Q_ACT_GELU_TANH>>(a, st, FP4Q_AMAX_WORK, parts);
 }
 
 }  // namespace

@@ -28,11 +28,11 @@ __global__ void __launch_bounds__(QTHREADS) token_amax_kernel(RowQuantArgs a, in
 cudaError_t launch_token_amax(int rot, const RowQuantArgs& a, int* parts, cudaStream_t st)
 {
     switch (rot) {
-    case 0: return launch_rows(token_amax_kernel<0>, a, st, FP4Q_AMAX_WORK, parts);
-    case 16: return launch_rows(token_amax_kernel<16>, a, st, FP4Q_AMAX_WORK, parts);
-    case 32: return launch_rows(token_amax_kernel<32>, a, st, FP4Q_AMAX_WORK, parts);
-    case 64: return launch_rows(token_amax_kernel<64>, a, st, FP4Q_AMAX_WORK, parts);
-    case 128: return launch_rows(token_amax_kernel<128>, a, st, FP4Q_AMAX_WORK, parts);
+    case 0: return launch_rows<token_amax_kernel<0>>(a, st, FP4Q_AMAX_WORK, parts);
+    case 16: return launch_rows<token_amax_kernel<16>>(a, st, FP4Q_AMAX_WORK, parts);
+    case 32: return launch_rows<token_amax_kernel<32>>(a, st, FP4Q_AMAX_WORK, parts);
+    case 64: return launch_rows<token_amax_kernel<64>>(a, st, FP4Q_AMAX_WORK, parts);
+    case 128: return launch_rows<token_amax_kernel<128>>(a, st, FP4Q_AMAX_WORK, parts);
     default: return cudaErrorInvalidValue;
     }
 }

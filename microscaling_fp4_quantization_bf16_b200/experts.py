@@ -18,6 +18,7 @@ that hold no choice are left as they were.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -50,16 +51,18 @@ class ExpertWeights:
     global_scale: Optional[torch.Tensor]  # float32 [experts] (NVFP4) or None
 
 
-def _need(t, name: str, dtype, *shape) -> None:
-    """t is a contiguous CUDA tensor of dtype (or one of several) and shape (None: any)."""
+def _need(t, name: str, device, dtype, *shape) -> None:
+    """t is a contiguous tensor on `device` of dtype (or one of several) and shape (None: any)."""
     try:
-        if (t.is_cuda and (t.dtype is dtype or t.dtype in dtype) and t.is_contiguous()
+        if (t.device == device and (t.dtype is dtype or t.dtype in dtype) and t.is_contiguous()
                 and (not shape or t.shape == shape)):
             return
     except (AttributeError, TypeError):
         pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"all tensors must be on {device}, {name} is on {t.device}")
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -69,9 +72,16 @@ def _need(t, name: str, dtype, *shape) -> None:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
-def _matrix(t, name: str, dtype):
-    """The shape of t, a contiguous CUDA matrix of dtype (or one of several)."""
-    _need(t, name, dtype)
+def _device(t, name: str) -> torch.device:
+    """The CUDA device of a call's first tensor, which all the others must share."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _matrix(t, name: str, device, dtype):
+    """The shape of t, a contiguous matrix on `device` of dtype (or one of several)."""
+    _need(t, name, device, dtype)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(shape)}")
@@ -120,29 +130,24 @@ def _call(name: str, device: torch.device, *args) -> None:
         _abi.fail(name, status)
 
 
-def _same_device(device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
-
-
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
 def _plan_args(plan: ExpertPlan, device) -> None:
-    _matrix(plan.slots, "plan.slots", torch.int32)
-    _same_device(device, plan.slots)
+    _matrix(plan.slots, "plan.slots", device, torch.int32)
     if plan.rows < 0 or plan.rows % SEGMENT_ROWS:
         raise ValueError(f"plan.rows must be a multiple of {SEGMENT_ROWS}, got {plan.rows}")
 
 
+@functools.lru_cache(maxsize=4096)
 def scale_bytes(rows: int, cols: int, fmt="nvfp4") -> int:
     """Bytes of the MMA-layout scales of [rows, cols] (0 rows or columns: 0)."""
     blocks = cols // (16 if _fmt(fmt) == 0 else 32)
     return -(-rows // 128) * 128 * (-(-blocks // 4) * 4)
 
 
+@functools.lru_cache(maxsize=4096)
 def expert_rows(choices: int, experts: int) -> int:
     """Rows of the padded layout that hold any routing of `choices` choices."""
     rows = _entry("fp4q_expert_rows")(choices, experts)
@@ -151,13 +156,18 @@ def expert_rows(choices: int, experts: int) -> int:
     return rows
 
 
+@functools.lru_cache(maxsize=4096)
+def _sort_work(choices: int, experts: int) -> int:
+    return _entry("fp4q_expert_sort_work")(choices, experts)
+
+
 def expert_sort(ids: torch.Tensor, experts: int, rows: Optional[int] = None,
                 out: Optional[ExpertPlan] = None) -> ExpertPlan:
     """Sorts the router's choices ids (int32 or int64 [tokens, k]) by expert,
     stably. An id outside 0 .. experts-1 drops the choice. rows: rows of the
     layout, at least the default expert_rows(tokens * k, experts)."""
-    _matrix(ids, "ids", (torch.int32, torch.int64))
-    dev = ids.device
+    dev = _device(ids, "ids")
+    _matrix(ids, "ids", dev, (torch.int32, torch.int64))
     n = ids.numel()
     least = expert_rows(n, experts)
     if out is None:
@@ -166,13 +176,12 @@ def expert_sort(ids: torch.Tensor, experts: int, rows: Optional[int] = None,
                          torch.empty(ids.shape, dtype=torch.int32, device=dev),
                          least if rows is None else rows)
     else:
-        _need(out.counts, "out.counts", torch.int32, experts)
-        _need(out.starts, "out.starts", torch.int32, experts + 1)
-        _need(out.slots, "out.slots", torch.int32, *ids.shape)
-        _same_device(dev, out.counts, out.starts, out.slots)
+        _need(out.counts, "out.counts", dev, torch.int32, experts)
+        _need(out.starts, "out.starts", dev, torch.int32, experts + 1)
+        _need(out.slots, "out.slots", dev, torch.int32, *ids.shape)
     if out.rows < least or out.rows % SEGMENT_ROWS:
         raise ValueError(f"rows must be a multiple of {SEGMENT_ROWS} and at least {least}, got {out.rows}")
-    size = _entry("fp4q_expert_sort_work")(n, experts)
+    size = _sort_work(n, experts)
     work = torch.empty(size // 4, dtype=torch.int32, device=dev) if size else None
     _call("fp4q_expert_sort", dev, ids.data_ptr(), ids.element_size(), n, experts,
           out.counts.data_ptr(), out.starts.data_ptr(), out.slots.data_ptr(), _ptr(work))
@@ -189,13 +198,12 @@ def _quantized_out(out, rows: int, cols: int, f: int, dq_dtype, device):
         return Quantized(new((rows, cols // 2), torch.uint8), new((size,), torch.uint8),
                          new((1,), torch.float32) if f == 0 else None, None,
                          new((rows, cols), dq_dtype) if dq_dtype is not None else None)
-    _need(out.codes, "out.codes", torch.uint8, rows, cols // 2)
-    _need(out.scales, "out.scales", torch.uint8, size)
+    _need(out.codes, "out.codes", device, torch.uint8, rows, cols // 2)
+    _need(out.scales, "out.scales", device, torch.uint8, size)
     if f == 0:
-        _need(out.global_scale, "out.global_scale", torch.float32, 1)
+        _need(out.global_scale, "out.global_scale", device, torch.float32, 1)
     if out.dq is not None:
-        _need(out.dq, "out.dq", (torch.float32, torch.bfloat16), rows, cols)
-    _same_device(device, out.codes, out.scales, out.global_scale, out.dq)
+        _need(out.dq, "out.dq", device, (torch.float32, torch.bfloat16), rows, cols)
     return out
 
 
@@ -204,8 +212,7 @@ def _amax_args(f: int, global_amax, device):
     if f != 0:
         return None, None
     if global_amax is not None:
-        _need(global_amax, "global_amax", torch.float32, 1)
-        _same_device(device, global_amax)
+        _need(global_amax, "global_amax", device, torch.float32, 1)
         return global_amax, None
     return None, torch.empty(AMAX_WORK, dtype=torch.float32, device=device)
 
@@ -218,8 +225,8 @@ def expert_quantize(x: torch.Tensor, plan: ExpertPlan, fmt="nvfp4", strategy="ab
     [plan.rows, cols] with MMA-layout scales (and dequantized values in
     .dq, if dq_dtype or out.dq asks for them). NVFP4 without global_amax takes the
     abs-max of x in an extra pass (see fp4q_expert_quantize for its s_g)."""
-    tokens, cols = _matrix(x, "x", torch.bfloat16)
-    dev = x.device
+    dev = _device(x, "x")
+    tokens, cols = _matrix(x, "x", dev, torch.bfloat16)
     _plan_args(plan, dev)
     if plan.slots.shape[0] != tokens:
         raise ValueError(f"x has {tokens} tokens, the plan {plan.slots.shape[0]}")
@@ -237,12 +244,12 @@ def expert_weights(w: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0
     """Quantizes bf16 weights [experts, N, K] for expert_gemm, each expert with
     its own scales (done once, when a model is loaded)."""
     from . import Quantized, quantize_mma
-    _need(w, "w", torch.bfloat16)
+    dev = _device(w, "w")
+    _need(w, "w", dev, torch.bfloat16)
     if w.dim() != 3:
         raise ValueError(f"w must have shape [experts, N, K], got {tuple(w.shape)}")
     experts, n, k = w.shape
     f = _fmt(fmt)
-    dev = w.device
     out = ExpertWeights(
         torch.empty(experts, n, k // 2, dtype=torch.uint8, device=dev),
         torch.zeros(experts, scale_bytes(n, k, f), dtype=torch.uint8, device=dev),
@@ -263,30 +270,28 @@ def expert_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scale: O
     -> [rows, N]. Operands as expert_quantize / glu_quantize and expert_weights
     return them."""
     f = _fmt(fmt)
-    _need(w_codes, "w_codes", torch.uint8)
+    dev = _device(w_codes, "w_codes")
+    _need(w_codes, "w_codes", dev, torch.uint8)
     if w_codes.dim() != 3:
         raise ValueError(f"w_codes must have shape [experts, N, K/2], got {tuple(w_codes.shape)}")
     experts, n, half = w_codes.shape
-    dev = w_codes.device
     k = 2 * half
     _plan_args(plan, dev)
     rows = plan.rows
-    _need(a_codes, "a_codes", torch.uint8, rows, half)
-    _need(a_scales, "a_scales", torch.uint8, scale_bytes(rows, k, f))
-    _need(w_scales, "w_scales", torch.uint8, experts, scale_bytes(n, k, f))
-    _need(plan.counts, "plan.counts", torch.int32, experts)
-    _need(plan.starts, "plan.starts", torch.int32, experts + 1)
+    _need(a_codes, "a_codes", dev, torch.uint8, rows, half)
+    _need(a_scales, "a_scales", dev, torch.uint8, scale_bytes(rows, k, f))
+    _need(w_scales, "w_scales", dev, torch.uint8, experts, scale_bytes(n, k, f))
+    _need(plan.counts, "plan.counts", dev, torch.int32, experts)
+    _need(plan.starts, "plan.starts", dev, torch.int32, experts + 1)
     if f == 0:
-        _need(a_global_scale, "a_global_scale", torch.float32, 1)
-        _need(w_global_scale, "w_global_scale", torch.float32, experts)
+        _need(a_global_scale, "a_global_scale", dev, torch.float32, 1)
+        _need(w_global_scale, "w_global_scale", dev, torch.float32, experts)
     else:
         a_global_scale = w_global_scale = None
     if out is None:
         out = torch.empty(rows, n, dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", (torch.float32, torch.bfloat16), rows, n)
-    _same_device(dev, a_codes, a_scales, a_global_scale, w_scales, w_global_scale, plan.counts,
-                 plan.starts, out)
+        _need(out, "out", dev, (torch.float32, torch.bfloat16), rows, n)
     choices = plan.slots.numel()
     _call("fp4q_expert_gemm", dev, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_global_scale),
           w_codes.data_ptr(), w_scales.data_ptr(), _ptr(w_global_scale), plan.counts.data_ptr(),
@@ -302,8 +307,9 @@ def glu_quantize(gu: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0,
     """Gated activation and quantize_mma() in one pass: gu bf16 [rows, 2 * cols]
     (gate, then value) -> Quantized of act(gate) * value. With a plan only the
     rows that hold a choice are taken, without one all rows."""
-    rows, cols = _matrix(gu, "gu", torch.bfloat16)
-    dev, cols, odd = gu.device, cols // 2, cols % 2
+    dev = _device(gu, "gu")
+    rows, cols = _matrix(gu, "gu", dev, torch.bfloat16)
+    cols, odd = cols // 2, cols % 2
     if odd:
         raise ValueError("gu must have an even number of columns")
     if plan is not None:
@@ -325,9 +331,10 @@ def glu_bwd(gu: torch.Tensor, dh: torch.Tensor, plan: Optional[ExpertPlan] = Non
             rot: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of glu_quantize's gate and value (bf16 [rows, 2 * cols]) from
     dh = dL/d(quantized values) bf16 [rows, cols], straight through the rounding."""
-    rows, cols = _matrix(gu, "gu", torch.bfloat16)
-    dev, cols, odd = gu.device, cols // 2, cols % 2
-    _need(dh, "dh", torch.bfloat16, rows, cols)
+    dev = _device(gu, "gu")
+    rows, cols = _matrix(gu, "gu", dev, torch.bfloat16)
+    cols, odd = cols // 2, cols % 2
+    _need(dh, "dh", dev, torch.bfloat16, rows, cols)
     if odd:
         raise ValueError("gu must have an even number of columns")
     if plan is not None:
@@ -337,8 +344,7 @@ def glu_bwd(gu: torch.Tensor, dh: torch.Tensor, plan: Optional[ExpertPlan] = Non
     if out is None:
         out = torch.empty_like(gu)
     else:
-        _need(out, "out", torch.bfloat16, rows, 2 * cols)
-    _same_device(dev, dh, out)
+        _need(out, "out", dev, torch.bfloat16, rows, 2 * cols)
     _call("fp4q_glu_bwd", dev, gu.data_ptr(), dh.data_ptr(), rows, cols,
           plan.slots.data_ptr() if plan is not None else None,
           plan.slots.numel() if plan is not None else rows, _act(act), rot, out.data_ptr())
@@ -351,19 +357,18 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
     """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: ones), then
     the rotation. Without weights and with the forward's rot it is the
     straight-through gradient of expert_quantize."""
-    rows, cols = _matrix(y, "y", (torch.float32, torch.bfloat16))
-    dev = y.device
+    dev = _device(y, "y")
+    rows, cols = _matrix(y, "y", dev, (torch.float32, torch.bfloat16))
     _plan_args(plan, dev)
     if rows != plan.rows:
         raise ValueError(f"y has {rows} rows, the plan {plan.rows}")
     tokens, k = plan.slots.shape
     if weights is not None:
-        _need(weights, "weights", torch.float32, tokens, k)
+        _need(weights, "weights", dev, torch.float32, tokens, k)
     if out is None:
         out = torch.empty(tokens, cols, dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", (torch.float32, torch.bfloat16), tokens, cols)
-    _same_device(dev, weights, out)
+        _need(out, "out", dev, (torch.float32, torch.bfloat16), tokens, cols)
     _call("fp4q_expert_combine", dev, y.data_ptr(), _DTYPES[y.dtype], plan.rows, cols,
           plan.slots.data_ptr(), tokens, k, _ptr(weights), rot, out.data_ptr(), _DTYPES[out.dtype])
     return out
@@ -374,23 +379,22 @@ def expert_combine_bwd(g: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
                        want_dweights: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Gradients of expert_combine (rot 0) from g = dL/dout: (dy of y's type
     and shape, dweights float32 [tokens, k] or None)."""
-    rows, cols = _matrix(y, "y", (torch.float32, torch.bfloat16))
-    dev = y.device
+    dev = _device(y, "y")
+    rows, cols = _matrix(y, "y", dev, (torch.float32, torch.bfloat16))
     _plan_args(plan, dev)
     if rows != plan.rows:
         raise ValueError(f"y has {rows} rows, the plan {plan.rows}")
     tokens, k = plan.slots.shape
-    _need(g, "g", (torch.float32, torch.bfloat16), tokens, cols)
+    _need(g, "g", dev, (torch.float32, torch.bfloat16), tokens, cols)
     if weights is not None:
-        _need(weights, "weights", torch.float32, tokens, k)
+        _need(weights, "weights", dev, torch.float32, tokens, k)
     if out is None:
         out = torch.empty_like(y)
     else:
-        _need(out, "out", y.dtype, plan.rows, cols)
+        _need(out, "out", dev, y.dtype, plan.rows, cols)
     dw = torch.empty(tokens, k, dtype=torch.float32, device=dev) if want_dweights else None
     if dw is not None and cols == 0:
         dw.zero_()
-    _same_device(dev, g, weights, out)
     _call("fp4q_expert_combine_bwd", dev, g.data_ptr(), _DTYPES[g.dtype], y.data_ptr(),
           _DTYPES[y.dtype], plan.rows, cols, plan.slots.data_ptr(), tokens, k, _ptr(weights),
           out.data_ptr(), _ptr(dw))

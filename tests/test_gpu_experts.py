@@ -697,6 +697,38 @@ def test_layer_captured_and_replayed(gpu, fmt):
     assert gpu.load().fp4q_device_errors() == 0
 
 
+def test_layers_on_two_streams(gpu):
+    """Two layers (one of long segments, one of short) on streams of their own, at the same time and with dense
+    products between them: each gives what it gives alone."""
+    cases = []
+    for tokens, fmt, seed in ((900, "nvfp4", 1), (40, "mxfp4", 2)):
+        k, experts, H, I = 2, 4, 512, 384
+        up = gpu.expert_weights(synth.gaussian(experts * 2 * I, H, seed=seed, std=0.05).reshape(experts, 2 * I, H).cuda(), fmt)
+        down = gpu.expert_weights(synth.gaussian(experts * H, I, seed=seed + 5, std=0.05).reshape(experts, H, I).cuda(), fmt)
+        x = synth.laplace_outliers(tokens, H, seed=seed).cuda()
+        ids = torch.from_numpy(ref.route(tokens, k, experts, seed)).cuda()
+        w = torch.rand(tokens, k, generator=torch.Generator().manual_seed(seed)).cuda()
+        q = gpu.quantize_mma(x, fmt)
+
+        def run(fmt=fmt, up=up, down=down, x=x, ids=ids, w=w, q=q, experts=experts):
+            out = layer(gpu, x, gpu.expert_sort(ids, experts), w, up, down, fmt, 0)[0]
+            gs = None if fmt == "mxfp4" else up.global_scale[:1]
+            return out, gpu.gemm(q.codes, q.scales, q.global_scale, up.codes[0], up.scales[0], gs, fmt)
+        cases.append(run)
+    want = [run() for run in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(20):
+        for run, stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                got.append(run())
+    torch.cuda.synchronize()
+    for i, (out, dense) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(dense, want[i % 2][1]), i
+    assert gpu.load().fp4q_device_errors() == 0
+
+
 def test_results_repeat(gpu):
     """The same call twice gives the same bits, products and gradients too."""
     tokens, k, experts, H, N = 3000, 4, 16, 512, 512
