@@ -266,11 +266,11 @@ __device__ __forceinline__ unsigned seg_amax(const float (&y)[SEG])
 }
 
 // CTAs per SM that the registers are held to: searches as the compiler likes,
-// else 5 for tokens (6: 203 against 184 us for 16384 x 8192 to two experts each) and 4 behind the
-// activation (5 spills: 204 against 190 us for 8192 x 14336, MXFP4 H128).
-template <int STRAT, bool GLU>
+// else 4 (16384 x 8192 to two experts each, 4-over-6: 182 us; 5: 186, 6: 205; behind the
+// activation, 8192 x 14336 MXFP4 H128: 184, 5 spills: 200, 3: 197).
+template <int STRAT>
 struct RowMinBlocks {
-    static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : (GLU ? 4 : 5);
+    static constexpr int value = STRAT == K_BRUTE_FORCE || STRAT == K_MX_BRUTE ? 1 : 4;
 };
 
 // ---------------------------------------------------------------- tokens
@@ -289,7 +289,7 @@ __device__ __forceinline__ void fetch_tokens(const RowQuantArgs& a, int64_t s0, 
 
 // Segment s of x is segment s % spr of token s / spr. Persistent CTAs.
 template <int B, int ROT, int STRAT>
-__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, false>::value)
+__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     token_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
@@ -578,7 +578,7 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
 }
 
 template <int B, int ROT, int STRAT, int ACT>
-__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT, true>::value)
+__global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     glu_quant_kernel(RowQuantArgs a, int64_t ntiles)
 {
     pdl_begin();
