@@ -20,13 +20,11 @@
 
 namespace fp4q {
 
-// One warp's shared memory: two buffers of 32 segments of IN bf16 inputs in
-// chunks of 8 values, and their codes and scale bytes.
-template <int B, int IN>
+// A warp's way from segments to chunks: 32 segments' codes and scale bytes.
+template <int B>
 struct WarpStage {
-    uint4 in[2][IN][32 * 4];
     uint4 codes[32];
-    __align__(4) uint8_t scales[32 * (SEG / B)];
+    uint32_t scales[32];
 };
 
 // Slot of chunk c (segment c / 4, part c % 4) in a buffer.
@@ -87,45 +85,88 @@ __device__ __forceinline__ int32_t row_of(const RowQuantArgs& a, int64_t i, int 
     return r < a.rows ? r : -1;
 }
 
-// Copies the staged segments of a warp to the rows row(j), j < k, of this lane's
-// segment (-1: none). All lanes take part.
+// One lane's quantized segment: its codes and scale bytes (block b at byte b).
+struct Segment {
+    uint4 q;
+    uint32_t scales;
+};
+
+// process_segment with a lane's own variables as its output.
+template <int B, int STRAT, int ROT>
+__device__ __forceinline__ Segment quantize_segment(float (&y)[SEG], uint32_t keep,
+                                                    const ScaleTables<STRAT>& tab)
+{
+    __align__(16) uint8_t codes[SEG / 2];
+    __align__(4) uint8_t scales[4] = {};
+    QuantArgs a;
+    a.x = nullptr;
+    a.n = 0;
+    a.amax = nullptr;
+    a.sg_out = nullptr;
+    a.codes = codes;
+    a.scales = scales;
+    a.mse = nullptr;
+    a.dq = nullptr;
+    a.dq_kind = 0;
+    a.keep = keep;
+    a.mma_spr = 0;
+    a.mma_atoms_k = 0;
+    process_segment<B, STRAT, ROT>(y, 0, SEG, a, tab);
+    Segment r;
+    r.q = *reinterpret_cast<const uint4*>(codes);
+    r.scales = *reinterpret_cast<const uint32_t*>(scales);
+    return r;
+}
+
+template <int STRAT>
+__device__ __forceinline__ float scale_value(const ScaleTables<STRAT>& tab, uint32_t byte)
+{
+    if constexpr (is_mx_strat(STRAT))
+        return pow2f((int)byte - 127);
+    else
+        return tab.S[byte];
+}
+
+// Stores the warp's segments to the rows row(j), j < k, of each lane's segment
+// (-1: none). All lanes take part.
 template <int B, int STRAT, class Rows>
-__device__ __forceinline__ void store_rows(const RowQuantArgs& a, const uint4* codes,
-                                           const uint8_t* scales, const ScaleTables<STRAT>& tab,
+__device__ __forceinline__ void store_rows(const RowQuantArgs& a, const Segment& sg,
+                                           WarpStage<B>& st, const ScaleTables<STRAT>& tab,
                                            int lane, const Place& at, Rows row)
 {
     constexpr int NB = SEG / B;      // blocks of a segment
     constexpr int QUAD = 4 / NB;     // segments of a 4-block group
-    const uint4 q = codes[lane];
     // Segments per row a multiple of QUAD: the groups of 4 blocks lie inside
     // the warp, and the first lane of each writes its 4 bytes at once.
     const bool whole = a.spr % QUAD == 0;
-    uint32_t quad = 0;
-    if (whole && lane % QUAD == 0)
-        quad = *reinterpret_cast<const uint32_t*>(scales + lane * NB);
+    uint32_t quad = sg.scales;
+#pragma unroll
+    for (int d = 1; d < QUAD; ++d)
+        quad |= __shfl_down_sync(0xFFFFFFFFu, sg.scales, d) << (8 * NB * d);
     uint4 o[4];
     if (a.dq_kind == 2) {
         // bf16 values: chunk 32 c + lane is 8 values of segment 8 c + lane / 4
+        st.codes[lane] = sg.q;
+        st.scales[lane] = sg.scales;
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint32_t byte = scales[(8 * c + lane / 4) * NB + lane % 4 * 8 / B];
-            float S, v[8];
-            if constexpr (is_mx_strat(STRAT))
-                S = pow2f((int)byte - 127);
-            else
-                S = tab.S[byte];
-            e2m1_unpack8(reinterpret_cast<const uint32_t*>(codes)[32 * c + lane], v);
+            const uint32_t bytes = st.scales[8 * c + lane / 4];
+            const float S = scale_value<STRAT>(tab, (bytes >> (8 * (lane % 4 * 8 / B))) & 0xFFu);
+            float v[8];
+            e2m1_unpack8(reinterpret_cast<const uint32_t*>(st.codes)[32 * c + lane], v);
             o[c].x = pack_bf16x2(__fmul_rn(v[0], S), __fmul_rn(v[1], S));
             o[c].y = pack_bf16x2(__fmul_rn(v[2], S), __fmul_rn(v[3], S));
             o[c].z = pack_bf16x2(__fmul_rn(v[4], S), __fmul_rn(v[5], S));
             o[c].w = pack_bf16x2(__fmul_rn(v[6], S), __fmul_rn(v[7], S));
         }
+        __syncwarp();
     }
     for (int j = 0; j < a.k; ++j) {
         const int32_t r = row(j);
         const int64_t seg = (int64_t)r * a.spr + at.p;
         if (r >= 0) {
-            reinterpret_cast<uint4*>(a.codes)[seg] = q;
+            reinterpret_cast<uint4*>(a.codes)[seg] = sg.q;
             const uint32_t kb = at.p * NB;
             uint8_t* dst = a.scales + ((int64_t)(r >> 7) * a.atoms_k + (kb >> 2)) * 512 +
                            16 * (r & 31) + 4 * ((r >> 5) & 3);
@@ -135,7 +176,7 @@ __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const uint4* c
             } else {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    dst[(kb & 3) + b] = scales[lane * NB + b];
+                    dst[(kb & 3) + b] = (uint8_t)(sg.scales >> (8 * b));
                 if (at.p == a.spr - 1)  // padding blocks of the row's last group
                     for (uint32_t b = (kb & 3) + NB; b < 4; ++b)
                         dst[b] = 0;
@@ -161,15 +202,11 @@ __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const uint4* c
         } else if (a.dq_kind == 1 && r >= 0) {
             // fp32 values (for checks and calibration on small layers): each lane its segment
             float4* dst = reinterpret_cast<float4*>(a.dq) + seg * (SEG / 4);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            const uint32_t w[4] = {sg.q.x, sg.q.y, sg.q.z, sg.q.w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint32_t byte = scales[lane * NB + c * 8 / B];
-                float S, v[8];
-                if constexpr (is_mx_strat(STRAT))
-                    S = pow2f((int)byte - 127);
-                else
-                    S = tab.S[byte];
+                const float S = scale_value<STRAT>(tab, (sg.scales >> (8 * (c * 8 / B))) & 0xFFu);
+                float v[8];
                 e2m1_unpack8(w[c], v);
                 dst[2 * c] = make_float4(__fmul_rn(v[0], S), __fmul_rn(v[1], S), __fmul_rn(v[2], S),
                                          __fmul_rn(v[3], S));
@@ -178,25 +215,6 @@ __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const uint4* c
             }
         }
     }
-}
-
-// The warp's buffer as the output of process_segment.
-__device__ __forceinline__ QuantArgs stage_args(const RowQuantArgs& a, uint4* codes, uint8_t* scales)
-{
-    QuantArgs q;
-    q.x = nullptr;
-    q.n = 0;
-    q.amax = nullptr;
-    q.sg_out = nullptr;
-    q.codes = reinterpret_cast<uint8_t*>(codes);
-    q.scales = scales;
-    q.mse = nullptr;
-    q.dq = nullptr;
-    q.dq_kind = 0;
-    q.keep = a.keep;
-    q.mma_spr = 0;
-    q.mma_atoms_k = 0;
-    return q;
 }
 
 // The NVFP4 tables of a CTA (see ScaleTables), from the calibrated abs-max, or
@@ -294,20 +312,21 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B, 1> stage[QTHREADS / 32];
+    __shared__ WarpStage<B> stage[QTHREADS / 32];
+    __shared__ uint4 inputs[QTHREADS / 32][2][32 * 4];
     const int lane = threadIdx.x & 31;
-    WarpStage<B, 1>& st = stage[threadIdx.x / 32];
-    const QuantArgs qa = stage_args(a, st.codes, st.scales);
+    WarpStage<B>& st = stage[threadIdx.x / 32];
+    uint4 (*in)[32 * 4] = inputs[threadIdx.x / 32];
     int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * QTHREADS;
-    fetch_tokens(a, s - lane, lane, st.in[0][0]);
+    fetch_tokens(a, s - lane, lane, in[0]);
     copies_commit();
     row_scale_tables<STRAT>(a, tab);
     Places places(a, s - lane, step);
     int buf = 0;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1, places.next(a)) {
         if (t + gridDim.x < ntiles)
-            fetch_tokens(a, s + step - lane, lane, st.in[buf ^ 1][0]);
+            fetch_tokens(a, s + step - lane, lane, in[buf ^ 1]);
         copies_commit();
         copies_wait_but_one();
         __syncwarp();
@@ -320,13 +339,12 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
             uint4 v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                v[k] = st.in[buf][0][slot_of(4 * lane + k)];
+                v[k] = in[buf][slot_of(4 * lane + k)];
             float y[SEG];
             unpack_seg<!is_mx_strat(STRAT)>(v, y);
             rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
-            process_segment<B, STRAT, ROT>(y, lane, SEG, qa, tab);
-            __syncwarp();
-            store_rows<B, STRAT>(a, st.codes, st.scales, tab, lane, at, [&](int j) {
+            const Segment sg = quantize_segment<B, STRAT, ROT>(y, a.keep, tab);
+            store_rows<B, STRAT>(a, sg, st, tab, lane, at, [&](int j) {
                 if (at.one && j < 32)
                     return __shfl_sync(0xFFFFFFFFu, mine, j);
                 return at.live ? row_of(a, at.i, j) : -1;
@@ -583,16 +601,15 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B, 2> stage[QTHREADS / 32];
+    __shared__ WarpStage<B> stage[QTHREADS / 32];
+    __shared__ uint4 inputs[QTHREADS / 32][2][2][32 * 4];
     const int lane = threadIdx.x & 31;
-    WarpStage<B, 2>& st = stage[threadIdx.x / 32];
-    const QuantArgs qa = stage_args(a, st.codes, st.scales);
+    WarpStage<B>& st = stage[threadIdx.x / 32];
     row_scale_tables<STRAT>(a, tab);
-    glu_tiles<ACT>(a, ntiles, lane, st.in, [&](float (&y)[SEG], const Place& at, int32_t row) {
+    glu_tiles<ACT>(a, ntiles, lane, inputs[threadIdx.x / 32], [&](float (&y)[SEG], const Place& at, int32_t row) {
         rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
-        process_segment<B, STRAT, ROT>(y, lane, SEG, qa, tab);
-        __syncwarp();
-        store_rows<B, STRAT>(a, st.codes, st.scales, tab, lane, at, [&](int) { return row; });
+        const Segment sg = quantize_segment<B, STRAT, ROT>(y, a.keep, tab);
+        store_rows<B, STRAT>(a, sg, st, tab, lane, at, [&](int) { return row; });
     });
 }
 
