@@ -83,7 +83,8 @@ fp4q_status fp4q_expert_sort(const void* ids, int id_bytes, int64_t n, int64_t e
  * fp4q_expert_quantize -- fp4q_quantize_mma of every token, written to the
  * rows of its choices: for a given abs-max (and for MXFP4) bit for bit the codes and scale
  * bytes that quantizing the gathered rows gives. A token is quantized once.
- * x            bf16 [tokens, cols]; cols a multiple of 32 and of rot.
+ * x            bf16 [tokens, cols]; cols a multiple of 32 and of rot, tokens *
+ *              cols / 32 at most 0xF0000000.
  * slots        int32 [tokens, k]; a value outside 0 .. rows-1 is skipped.
  * rows         rows of the outputs, a multiple of 128.
  * fmt, strat, rot as fp4q_quantize_mma (NVFP4 block 16, MXFP4 block 32).
@@ -145,8 +146,8 @@ fp4q_status fp4q_expert_gemm(const uint8_t* a_codes, const uint8_t* a_mma_scales
  * slots, n     int32 [n]: the rows to take (a value outside 0 .. rows-1 is skipped;
  *              a row named twice is written twice with the same bits), or
  *              NULL for all rows (n is ignored).
- * cols         a multiple of 32 and of rot; other arguments as
- *              fp4q_expert_quantize. global_amax_in NULL (NVFP4) takes the
+ * cols         a multiple of 32 and of rot (rows taken * cols / 32 at most
+ *              0xF0000000); other arguments as fp4q_expert_quantize. global_amax_in NULL (NVFP4) takes the
  *              abs-max of the rotated h over the rows taken, and s_g from it as there. Without slots,
  *              rows may be any number and mma_scales has
  *              fp4q_mma_scale_bytes(rows, cols, fmt) bytes.

@@ -27,7 +27,8 @@ struct WarpStage {
     uint32_t scales[32];
 };
 
-// Slot of chunk c (segment c / 4, part c % 4) in a buffer.
+// Slot of chunk c (segment c / 4, part c % 4) in a buffer. Chunks 32 apart are
+// 32 slots apart.
 __device__ __forceinline__ int slot_of(int c) { return c ^ ((c >> 3) & 3); }
 
 __device__ __forceinline__ void copy16(uint4* dst, const uint4* src, bool real)
@@ -49,13 +50,13 @@ struct Place {
 };
 
 // The places of a warp's tiles, a grid's step apart: the division is done once,
-// a step adds its quotient and remainder.
+// a step adds its quotient and remainder. (Segment numbers and what a grid's
+// step or two add to them stay below 2^32: the host checks.)
 struct Places {
     uint32_t i0, p0, di, dp;  // row and segment of the warp's first lane; the step
 
-    __device__ __forceinline__ Places(const RowQuantArgs& a, int64_t s0, int64_t step)
-        : i0((uint32_t)s0 / a.spr), p0((uint32_t)s0 - i0 * a.spr), di((uint32_t)step / a.spr),
-          dp((uint32_t)step - di * a.spr)
+    __device__ __forceinline__ Places(const RowQuantArgs& a, uint32_t s0, uint32_t step)
+        : i0(s0 / a.spr), p0(s0 - i0 * a.spr), di(step / a.spr), dp(step - di * a.spr)
     {
     }
     __device__ __forceinline__ void next(const RowQuantArgs& a)
@@ -67,13 +68,15 @@ struct Places {
             ++i0;
         }
     }
-    __device__ __forceinline__ Place at(const RowQuantArgs& a, int lane, bool live) const
+    __device__ __forceinline__ Place at(const RowQuantArgs& a, int lane) const
     {
-        Place r{i0, p0 + lane, live, p0 + 32 <= a.spr};
-        while (r.p >= a.spr) {  // a warp that spans rows
-            r.p -= a.spr;
-            ++r.i;
-        }
+        Place r{i0, p0 + lane, true, p0 + 32 <= a.spr};
+        if (!r.one)  // a warp that spans rows
+            while (r.p >= a.spr) {
+                r.p -= a.spr;
+                ++r.i;
+            }
+        r.live = r.i < a.n;
         return r;
     }
 };
@@ -294,21 +297,27 @@ struct RowMinBlocks {
 // ---------------------------------------------------------------- tokens
 
 // Starts the copies of the warp's 32 segments from segment s0 of x.
-__device__ __forceinline__ void fetch_tokens(const RowQuantArgs& a, int64_t s0, int lane, uint4* in)
+__device__ __forceinline__ void fetch_tokens(const RowQuantArgs& a, uint32_t s0, int lane, uint4* in)
 {
-    const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
+    const uint4* x4 = reinterpret_cast<const uint4*>(a.x) + (uint64_t)s0 * 4 + lane;
+    uint4* dst = in + slot_of(lane);
+    if (s0 + 32 <= a.nseg) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int64_t at = s0 * 4 + 32 * c + lane;
-        const bool real = at < 4 * a.nseg;
-        copy16(in + slot_of(32 * c + lane), x4 + (real ? at : 0), real);
+        for (int c = 0; c < 4; ++c)
+            copy16(dst + 32 * c, x4 + 32 * c, true);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const bool real = s0 + 8 * c + lane / 4 < a.nseg;
+            copy16(dst + 32 * c, real ? x4 + 32 * c : reinterpret_cast<const uint4*>(a.x), real);
+        }
     }
 }
 
 // Segment s of x is segment s % spr of token s / spr. Persistent CTAs.
 template <int B, int ROT, int STRAT>
 __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
-    token_quant_kernel(RowQuantArgs a, int64_t ntiles)
+    token_quant_kernel(RowQuantArgs a, uint32_t ntiles)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
@@ -317,21 +326,22 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
     const int lane = threadIdx.x & 31;
     WarpStage<B>& st = stage[threadIdx.x / 32];
     uint4 (*in)[32 * 4] = inputs[threadIdx.x / 32];
-    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
-    const int64_t step = (int64_t)gridDim.x * QTHREADS;
-    fetch_tokens(a, s - lane, lane, in[0]);
+    const uint32_t step = gridDim.x * QTHREADS;
+    uint32_t s0 = blockIdx.x * QTHREADS + (threadIdx.x & ~31u);  // the warp's first segment
+    fetch_tokens(a, s0, lane, in[0]);
     copies_commit();
     row_scale_tables<STRAT>(a, tab);
-    Places places(a, s - lane, step);
+    Places places(a, s0, step);
     int buf = 0;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1, places.next(a)) {
+    for (uint32_t t = blockIdx.x; t < ntiles; t += gridDim.x, buf ^= 1, places.next(a)) {
+        s0 += step;
         if (t + gridDim.x < ntiles)
-            fetch_tokens(a, s + step - lane, lane, in[buf ^ 1]);
+            fetch_tokens(a, s0, lane, in[buf ^ 1]);
         copies_commit();
         copies_wait_but_one();
         __syncwarp();
-        if (s - lane < a.nseg) {  // warp-uniform
-            const Place at = places.at(a, lane, s < a.nseg);
+        if (places.i0 < a.n) {  // warp-uniform
+            const Place at = places.at(a, lane);
             // the rows of the first 32 choices, one a lane, on their way during the arithmetic
             int32_t mine = -1;
             if (at.one && lane < a.k)
@@ -523,24 +533,25 @@ __device__ __forceinline__ void fetch_glu(const RowQuantArgs& a, const Place& at
                                           uint4 (*in)[32 * 4])
 {
     const uint4* x4 = reinterpret_cast<const uint4*>(a.x);
-    if (at.one) {
-        const bool real = row >= 0;
-        const uint4* g = x4 + (real ? ((int64_t)row * 2 * a.spr + (at.p - lane)) * 4 + lane : 0);
-        const uint4* u = g + (real ? (int64_t)a.spr * 4 : 0);
-        const int more = real ? 32 : 0;
+    uint4* gate = in[0] + slot_of(lane);
+    uint4* value = in[1] + slot_of(lane);
+    if (at.one && row >= 0) {
+        const uint4* g = x4 + ((int64_t)row * 2 * a.spr + (at.p - lane)) * 4 + lane;
+        const uint4* u = g + (int64_t)a.spr * 4;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            copy16(in[0] + slot_of(32 * c + lane), g + c * more, real);
-            copy16(in[1] + slot_of(32 * c + lane), u + c * more, real);
+            copy16(gate + 32 * c, g + 32 * c, true);
+            copy16(value + 32 * c, u + 32 * c, true);
         }
     } else {
+        // (of a warp whose row is one and not there, every lane comes here)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int32_t r = __shfl_sync(0xFFFFFFFFu, row, 8 * c + lane / 4);
             const uint32_t p = __shfl_sync(0xFFFFFFFFu, at.p, 8 * c + lane / 4);
-            const int64_t base = r >= 0 ? ((int64_t)r * 2 * a.spr + p) * 4 + lane % 4 : 0;
-            copy16(in[0] + slot_of(32 * c + lane), x4 + base, r >= 0);
-            copy16(in[1] + slot_of(32 * c + lane), x4 + (r >= 0 ? base + (int64_t)a.spr * 4 : 0), r >= 0);
+            const uint4* g = x4 + (r >= 0 ? ((int64_t)r * 2 * a.spr + p) * 4 + lane % 4 : 0);
+            copy16(gate + 32 * c, g, r >= 0);
+            copy16(value + 32 * c, g + (r >= 0 ? (int64_t)a.spr * 4 : 0), r >= 0);
         }
     }
 }
@@ -548,41 +559,29 @@ __device__ __forceinline__ void fetch_glu(const RowQuantArgs& a, const Place& at
 // Walks a warp over its tiles of taken rows: the copies of the next tile are in flight, and
 // the row numbers of the one after it, while body(y, place, row) works on the current one.
 template <int ACT, class Body>
-__device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles, int lane,
+__device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, uint32_t ntiles, int lane,
                                           uint4 (*in)[2][32 * 4], Body body)
 {
-    const int64_t step = (int64_t)gridDim.x * QTHREADS;
-    int64_t s = (int64_t)blockIdx.x * QTHREADS + threadIdx.x;
     auto row_at = [&](const Place& at) { return at.live ? row_of(a, at.i, 0) : -1; };
-    Places places(a, s - lane, step);
-    Place now = places.at(a, lane, s < a.nseg);
+    Places places(a, blockIdx.x * QTHREADS + (threadIdx.x & ~31u), gridDim.x * QTHREADS);
+    Place now = places.at(a, lane);
     int32_t row = row_at(now);
     fetch_glu(a, now, row, lane, in[0]);
     copies_commit();
-    bool more = blockIdx.x + (int64_t)gridDim.x < ntiles;
-    Place next = now;
-    int32_t next_row = -1;
-    if (more) {
-        places.next(a);
-        next = places.at(a, lane, s + step < a.nseg);
-        next_row = row_at(next);
-    }
+    places.next(a);
+    Place next = places.at(a, lane);  // (past the last tile: not live, no row, no copy)
+    int32_t next_row = row_at(next);
     int buf = 0;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, s += step, buf ^= 1) {
-        Place then = next;
-        int32_t then_row = -1;
-        if (more)
+    for (uint32_t t = blockIdx.x; t < ntiles; t += gridDim.x, buf ^= 1) {
+        if (t + gridDim.x < ntiles)
             fetch_glu(a, next, next_row, lane, in[buf ^ 1]);
         copies_commit();
-        more = t + 2 * (int64_t)gridDim.x < ntiles;
-        if (more) {
-            places.next(a);
-            then = places.at(a, lane, s + 2 * step < a.nseg);
-            then_row = row_at(then);
-        }
+        places.next(a);
+        const Place then = places.at(a, lane);
+        const int32_t then_row = row_at(then);
         copies_wait_but_one();
         __syncwarp();
-        if (s - lane < a.nseg) {  // warp-uniform
+        if (__any_sync(0xFFFFFFFFu, now.live)) {
             float y[SEG];
             glu_segment<ACT>(in[buf][0], in[buf][1], lane, y);
             body(y, now, row);
@@ -597,7 +596,7 @@ __device__ __forceinline__ void glu_tiles(const RowQuantArgs& a, int64_t ntiles,
 
 template <int B, int ROT, int STRAT, int ACT>
 __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
-    glu_quant_kernel(RowQuantArgs a, int64_t ntiles)
+    glu_quant_kernel(RowQuantArgs a, uint32_t ntiles)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
@@ -614,38 +613,39 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 }
 
 // Resident CTAs per SM of one kernel (a template value, so that each kernel
-// keeps its own), queried once per process, times the SMs of the current device.
+// keeps its own), queried once per process; -1 if the query fails.
 template <auto KERNEL>
-int64_t resident_rows()
+int resident_rows()
 {
     static std::atomic<int> per_sm{0};
-    int dev = 0, sms = 0, n = per_sm.load(std::memory_order_relaxed);
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return -1;
+    int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, QTHREADS, 0) != cudaSuccess)
             return -1;
         n = n < 1 ? 1 : n;
         per_sm.store(n, std::memory_order_relaxed);
     }
-    return (int64_t)sms * n;
+    return n;
 }
 
-// Launch of a row quantize kernel over the resident CTAs, at most `most`.
+// Launch of a row quantize kernel over the resident CTAs, at most `most` (then
+// as many on every SM); their number goes to *ctas.
 template <auto KERNEL>
 cudaError_t launch_rows(const RowQuantArgs& a, cudaStream_t st, int64_t most = 0x7FFFFFFF,
                         int* ctas = nullptr)
 {
-    const int64_t nblk = (a.nseg + QTHREADS - 1) / QTHREADS;
-    const int64_t res = resident_rows<KERNEL>();
-    if (res < 0)
+    const int64_t nblk = ((int64_t)a.nseg + QTHREADS - 1) / QTHREADS;
+    int dev = 0, sms = 0;
+    int64_t per_sm = resident_rows<KERNEL>();
+    if (per_sm < 0 || cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms > most)
         return cudaErrorUnknown;
-    int64_t grid = nblk < res ? nblk : res;
-    grid = grid < most ? grid : most;
+    if (per_sm * sms > most)
+        per_sm = most / sms;
+    const int64_t grid = nblk < per_sm * sms ? nblk : per_sm * sms;
     if (ctas != nullptr)
         *ctas = (int)grid;
-    return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(QTHREADS), 0, st, a, nblk);
+    return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(QTHREADS), 0, st, a, (uint32_t)nblk);
 }
 
 #define FP4Q_ROWS_CASE(KERNEL_, B_, S_, R_) \

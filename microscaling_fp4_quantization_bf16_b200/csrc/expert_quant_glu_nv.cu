@@ -6,7 +6,7 @@ namespace fp4q {
 namespace {
 
 template <int ROT, int ACT>
-__global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, int64_t ntiles)
+__global__ void __launch_bounds__(QTHREADS) glu_amax_kernel(RowQuantArgs a, uint32_t ntiles)
 {
     pdl_begin();
     const int lane = threadIdx.x & 31;

@@ -51,11 +51,15 @@ struct SortArgs {
 int64_t sort_blocks(int64_t n);
 cudaError_t launch_expert_sort(const SortArgs& a, int id_bytes, cudaStream_t st);
 
+// Segments of a row quantizer's call: room for a few grid steps below 2^32.
+constexpr int64_t kMaxSegs = 0xF0000000ll;
+
 // Rows quantized into the MMA layout, from tokens (k destinations each) or
 // from the gated activation of rows (one destination).
 struct RowQuantArgs {
     const uint16_t* x;      // bf16 tokens [n, cols], or gate and value [rows, 2 cols]
-    int64_t nseg;           // 32-element segments: (tokens or rows taken) * spr, < 2^32
+    uint32_t n;             // tokens, or rows taken
+    uint32_t nseg;          // 32-element segments: n * spr, at most kMaxSegs
     uint32_t spr;           // segments per row = cols / 32
     uint32_t atoms_k;       // 4-block atoms per 128 rows along a row
     const int32_t* slots;   // [n, k] destination rows; NULL: row i itself (glu only)

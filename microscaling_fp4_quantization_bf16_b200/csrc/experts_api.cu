@@ -63,7 +63,8 @@ RowQuantArgs row_args(const void* x, int64_t count, int64_t rows, int64_t cols, 
     RowQuantArgs a;
     a.x = static_cast<const uint16_t*>(x);
     a.spr = (uint32_t)(cols / 32);
-    a.nseg = count * (cols / 32);
+    a.n = (uint32_t)count;
+    a.nseg = (uint32_t)(count * (cols / 32));
     const int block = fmt == FP4Q_FMT_NVFP4 ? 16 : 32;
     a.atoms_k = (uint32_t)((cols / block + 3) / 4);
     a.slots = slots;
@@ -144,7 +145,7 @@ fp4q_status fp4q_expert_quantize(const void* x, int64_t tokens, int64_t cols, in
     if (st != FP4Q_OK)
         return st;
     if (k < 1 || k > FP4Q_MAX_CHOICES || rows % kSegRows != 0 || !valid_size(tokens, cols) ||
-        tokens * (cols / 32) > 0xFFFFFFFFll)
+        tokens * (cols / 32) > kMaxSegs)
         return FP4Q_ERR_SHAPE;
     const int64_t n = tokens * cols;
     if (n > 0 && (x == nullptr || slots == nullptr))
@@ -233,7 +234,7 @@ fp4q_status fp4q_glu_quantize(const void* gu, int64_t rows, int64_t cols, const 
     if (st != FP4Q_OK)
         return st;
     const int64_t taken = slots == nullptr ? rows : n;
-    if (!valid_size(rows, 2 * cols) || !valid_size(taken, cols) || taken * (cols / 32) > 0xFFFFFFFFll)
+    if (!valid_size(rows, 2 * cols) || !valid_size(taken, cols) || taken * (cols / 32) > kMaxSegs)
         return FP4Q_ERR_SHAPE;
     const bool empty = taken == 0 || rows == 0 || cols == 0;
     if (!empty && (gu == nullptr || codes == nullptr || mma_scales == nullptr))
