@@ -192,7 +192,7 @@ fp4q_status fp4q_expert_combine(const void* y, fp4q_dtype y_dtype, int64_t rows,
 /*
  * fp4q_expert_combine_bwd -- gradients of fp4q_expert_combine (rot 0):
  * dy[slots[t, j]] = weights[t, j] * g[t] (one rounding), dweights[t, j] =
- * <g[t], y[slots[t, j]]> in fp32 (0 for a dropped choice).
+ * <g[t], y[slots[t, j]]>, summed in 64 bits and rounded once (0 for a dropped choice).
  * g            [tokens, cols] of g_dtype; y, dy [rows, cols] of y_dtype. y and
  *              dweights may both be NULL, to leave dweights out; weights NULL counts as
  *              ones. Rows of dy without a choice stay as they were.

@@ -4,7 +4,8 @@
 //
 // All are bound by memory: every value is read or written once, in 16-byte
 // pieces of 8 values a thread, neighbouring threads on neighbouring pieces, so
-// a warp's access covers 512 contiguous bytes. Sums are fp32 in a fixed order.
+// a warp's access covers 512 contiguous bytes. Sums run in a fixed order, in fp32, the router's
+// gradient in 64 bits.
 // A blockwise rotation (gradients are linear in it) runs on this layout: three
 // butterfly stages inside a thread's 8 values, the others between lanes.
 #include "experts.h"
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(CTHREADS) combine_kernel(CombineArgs a)
 
 // One block: one token. Each thread walks the token's columns 8 at a time:
 // one read of g, one of each choice's row, one write of each choice's
-// gradient; the products with y stay in one accumulator per choice. Four choices
+// gradient; the products with y stay in one 64-bit accumulator per choice (a
+// router's gradient is one number out of thousands of terms that may cancel; it costs 1 us of 47). Four choices
 // at a time: more of them in flight cost registers and thereby warps (4000 tokens x 4096 to four
 // experts: 52 us; 8 choices 67, two pieces of columns as well 61, both 104).
 template <bool G32, bool Y32>
@@ -157,12 +159,13 @@ __global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
 {
     constexpr int GROUP = 4;
     pdl_begin();
-    __shared__ float part[GROUP][CTHREADS / 32];
+    __shared__ double part[GROUP][CTHREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int64_t t = blockIdx.x;
     for (int j0 = 0; j0 < a.k; j0 += GROUP) {
         int32_t r[GROUP];
-        float w[GROUP], acc[GROUP];
+        float w[GROUP];
+        double acc[GROUP];
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) {
             const bool in = j0 + j < a.k;
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
             w[j] = in && a.weights != nullptr ? a.weights[t * a.k + j0 + j] : 1.0f;
             if (r[j] >= a.rows)
                 r[j] = -1;
-            acc[j] = 0.0f;
+            acc[j] = 0.0;
         }
         for (int64_t c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {
             Piece<Y32> p[GROUP];
@@ -191,7 +194,10 @@ __global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
                         widen8<Y32>(p[j], v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            acc[j] = __fmaf_rn(g[e], v[e], acc[j]);
+                            if constexpr (G32 || Y32)
+                                acc[j] = __fma_rn((double)g[e], (double)v[e], acc[j]);
+                            else  // the product of two bf16 numbers is exact in fp32
+                                acc[j] = __dadd_rn(acc[j], (double)__fmul_rn(g[e], v[e]));
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -204,16 +210,16 @@ __global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
             for (int j = 0; j < GROUP; ++j) {
 #pragma unroll
                 for (int d = 16; d > 0; d /= 2)
-                    acc[j] = __fadd_rn(acc[j], __shfl_xor_sync(0xFFFFFFFFu, acc[j], d));
+                    acc[j] = __dadd_rn(acc[j], __shfl_xor_sync(0xFFFFFFFFu, acc[j], d));
                 if (lane == 0)
                     part[j][warp] = acc[j];
             }
             __syncthreads();
             if (threadIdx.x < GROUP && j0 + (int)threadIdx.x < a.k) {
-                float s = 0.0f;
+                double s = 0.0;
                 for (int x = 0; x < warps; ++x)
-                    s = __fadd_rn(s, part[threadIdx.x][x]);
-                a.dw[t * a.k + j0 + threadIdx.x] = s;
+                    s = __dadd_rn(s, part[threadIdx.x][x]);
+                a.dw[t * a.k + j0 + threadIdx.x] = (float)s;
             }
             if (j0 + GROUP < a.k)
                 __syncthreads();

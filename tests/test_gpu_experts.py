@@ -389,10 +389,26 @@ def test_combine_gradient(gpu, g32, y32, tokens, k, experts, cols):
     wd = np.zeros((tokens, k))
     wd[t, j] = part.sum(1)
     bd = np.zeros((tokens, k))
-    bd[t, j] = cols * U24 * np.abs(part).sum(1)
+    bd[t, j] = U24 * np.abs(part.sum(1)) + cols * 2.0 ** -52 * np.abs(part).sum(1)   # 64 bits, rounded once
     assert (np.abs(dw.double().cpu().numpy() - wd) <= bd).all()
     same, none = gpu.expert_combine_bwd(g.cuda(), y.cuda(), p, w.cuda(), want_dweights=False)
     assert none is None and torch.equal(same[torch.from_numpy(r).cuda()], dy[torch.from_numpy(r).cuda()])
+
+
+def test_combine_gradient_that_cancels(gpu):
+    """A router's gradient that is a millionth of its terms keeps its digits."""
+    cols = 4096
+    p = plan_of(gpu, np.zeros((1, 1), np.int64), 1)
+    rng = np.random.default_rng(3)
+    g = torch.from_numpy(rng.standard_normal((1, cols))).to(torch.bfloat16)
+    y = torch.zeros(p.rows, cols, dtype=torch.bfloat16)
+    y[0] = torch.from_numpy(rng.standard_normal(cols)).to(torch.bfloat16)
+    y[0, cols // 2:] = -y[0, :cols // 2] * 1.0
+    g[0, cols // 2:] = g[0, :cols // 2]
+    y[0, 7] *= 1 + 2.0 ** -7
+    want = (ref.to64(g)[0] * ref.to64(y)[0]).sum()
+    _, dw = gpu.expert_combine_bwd(g.cuda(), y.cuda(), p)
+    assert want != 0 and abs(dw.item() - want) <= U24 * abs(want) + cols * 2.0 ** -52 * cols
 
 
 def test_combine_gradient_against_differences(gpu):
