@@ -254,17 +254,28 @@ __device__ __forceinline__ bool elect_one()
 // CTAs running together share the weights.
 struct Walk {
     const int32_t* prefix;  // shared: token tiles of the experts before e
-    int wtiles, e;
+    int experts, wtiles, e;
     int64_t total;
 
-    __device__ __forceinline__ Walk(const int32_t* p, int experts, int wt)
-        : prefix(p), wtiles(wt), e(0), total((int64_t)p[experts] * wt)
+    __device__ __forceinline__ Walk(const int32_t* p, int ex, int wt)
+        : prefix(p), experts(ex), wtiles(wt), e(0), total((int64_t)p[ex] * wt)
     {
     }
+    // item < total, not before the last one
     __device__ __forceinline__ void at(int64_t item, int& wtile, int& ttile)
     {
-        while (item >= (int64_t)prefix[e + 1] * wtiles)
-            ++e;
+        // first expert whose tiles end behind item
+        int lo = e, hi = experts - 1;
+        if (item < (int64_t)prefix[lo + 1] * wtiles)
+            hi = lo;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (item < (int64_t)prefix[mid + 1] * wtiles)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        e = lo;
         const int tt = prefix[e + 1] - prefix[e];
         const int idx = (int)(item - (int64_t)prefix[e] * wtiles);
         wtile = idx / tt;
@@ -328,20 +339,21 @@ __global__ void __launch_bounds__(GTHREADS, 1)
         }
     }
     pdl_begin();
+    // Token tiles of each expert, then of the experts before it; segments outside
+    // the buffer count none, and all together no more than disjoint segments can have.
+    for (int e = threadIdx.x; e < p.experts; e += GTHREADS) {
+        const int64_t c = p.counts[e], s = p.starts[e];
+        prefix[e + 1] = c > 0 && s >= 0 && s % kSegRows == 0 && s + c <= p.rows ? (int)((c + TN - 1) / TN) : 0;
+    }
+    if (threadIdx.x == 0)
+        prefix[0] = 0;
+    __syncthreads();
     if (warp == 0) {
-        // Token tiles of the experts before each; segments outside the buffer
-        // count none, and all together no more than disjoint segments can have.
         const int limit = (int)(p.rows / kSegRows);
         int carry = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
-            int t = 0;
-            if (e < p.experts) {
-                const int64_t c = p.counts[e], s = p.starts[e];
-                if (c > 0 && s >= 0 && s % kSegRows == 0 && s + c <= p.rows)
-                    t = (int)((c + TN - 1) / TN);
-            }
-            int inc = t;
+            int inc = e < p.experts ? prefix[e + 1] : 0;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
@@ -352,8 +364,6 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                 prefix[e + 1] = inc;
             carry = __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
-        if (lane == 0)
-            prefix[0] = 0;
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
