@@ -8,11 +8,21 @@
 // Memory: each warp brings its next 32 segments (2 KB of bf16, twice that for
 // gate and value) into shared memory with 16-byte asynchronous copies while it
 // works on the current ones, 512 contiguous bytes a copy instruction (chunk c of
-// segment s at slot c ^ (s / 2 % 4) of its four, so that reading a segment a lane is free of
-// bank conflicts too). No register holds a byte in flight. process_segment writes its codes and scale bytes
-// to the warp's buffer (its pointers are generic); from there a segment goes to each of
-// its token's rows. The dequantized values are formed from the staged codes by
-// the lane that stores them, again 512 contiguous bytes an instruction.
+// segment s at slot c ^ (s / 2 % 4) of its four, so that reading a segment a
+// lane is free of bank conflicts too). No register holds a byte in flight.
+// process_segment leaves its codes and scale bytes in registers (its output
+// pointers are a lane's own variables); from there a segment goes to each of its
+// token's rows. Dequantized values, where they are wanted, are formed by the
+// lane that stores them, from codes that pass through shared memory, again 512
+// contiguous bytes an instruction. (One lane to a segment for loads and stores, 64
+// bytes apart: 215 against 205 us for the activation of 8192 x 14336, 196
+// against 188 for 16384 x 8192 tokens to two experts each.)
+//
+// Bound by: with values written, tokens by memory (16384 x 8192 to two experts
+// each, 4-over-6: 936 MB in 184 us, 5.1 TB/s, seven tenths writes); without,
+// by instruction issue (133 us for one expert each); behind the activation by
+// instruction issue (7946 x 14336, MXFP4 H128, values: 744 MB in 168 us, about 34
+// instructions a value at 0.66 per scheduler and clock).
 #pragma once
 
 #include "experts.h"
@@ -21,7 +31,6 @@
 namespace fp4q {
 
 // A warp's way from segments to chunks: 32 segments' codes and scale bytes.
-template <int B>
 struct WarpStage {
     uint4 codes[32];
     uint32_t scales[32];
@@ -134,7 +143,7 @@ __device__ __forceinline__ float scale_value(const ScaleTables<STRAT>& tab, uint
 // (-1: none). All lanes take part.
 template <int B, int STRAT, class Rows>
 __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const Segment& sg,
-                                           WarpStage<B>& st, const ScaleTables<STRAT>& tab,
+                                           WarpStage& st, const ScaleTables<STRAT>& tab,
                                            int lane, const Place& at, Rows row)
 {
     constexpr int NB = SEG / B;      // blocks of a segment
@@ -321,10 +330,10 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B> stage[QTHREADS / 32];
+    __shared__ WarpStage stage[QTHREADS / 32];
     __shared__ uint4 inputs[QTHREADS / 32][2][32 * 4];
     const int lane = threadIdx.x & 31;
-    WarpStage<B>& st = stage[threadIdx.x / 32];
+    WarpStage& st = stage[threadIdx.x / 32];
     uint4 (*in)[32 * 4] = inputs[threadIdx.x / 32];
     const uint32_t step = gridDim.x * QTHREADS;
     uint32_t s0 = blockIdx.x * QTHREADS + (threadIdx.x & ~31u);  // the warp's first segment
@@ -600,10 +609,10 @@ __global__ void __launch_bounds__(QTHREADS, RowMinBlocks<STRAT>::value)
 {
     pdl_begin();
     __shared__ ScaleTables<STRAT> tab;
-    __shared__ WarpStage<B> stage[QTHREADS / 32];
+    __shared__ WarpStage stage[QTHREADS / 32];
     __shared__ uint4 inputs[QTHREADS / 32][2][2][32 * 4];
     const int lane = threadIdx.x & 31;
-    WarpStage<B>& st = stage[threadIdx.x / 32];
+    WarpStage& st = stage[threadIdx.x / 32];
     row_scale_tables<STRAT>(a, tab);
     glu_tiles<ACT>(a, ntiles, lane, inputs[threadIdx.x / 32], [&](float (&y)[SEG], const Place& at, int32_t row) {
         rotate_seg<ROT, !foldable<ROT, STRAT>()>(y, lane);
