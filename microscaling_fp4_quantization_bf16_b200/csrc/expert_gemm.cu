@@ -33,7 +33,8 @@
 // the 48 columns that both share have been read.
 //
 // Waits are bounded: one that runs out raises the CTA's abort flag and the
-// device error counter, and every role leaves after its copies have landed.
+// device error counter, and every role leaves after its copies have landed and its
+// products have ended.
 #include "experts.h"
 #include "fp4q_device.cuh"
 
@@ -429,6 +430,10 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                 __syncwarp();
             }
         }
+        // The releases of the last stages are arrivals of commits that nothing above waits for,
+        // a pair's in both CTAs: they land before the memory of their barriers is given back.
+        for (int j = it < T::STAGES ? 0 : it - T::STAGES; ok && j < it; ++j)
+            ok = bar_wait(empty(j % T::STAGES), (j / T::STAGES) & 1, abort_flag);
         if (!ok) {
             if (lane == 0)
                 atomicAdd(p.err, 1u);
@@ -502,8 +507,15 @@ __global__ void __launch_bounds__(GTHREADS, 1)
             if (ok && leader)
                 commit<PAIR>(acc_full(buf));
         }
-        if (!ok && lane == 0)
-            atomicAdd(p.err, 1u);
+        if (!ok) {
+            if (lane == 0)
+                atomicAdd(p.err, 1u);
+            // products in flight end before their memory is given back
+            const int j = it - 1;
+            for (uint32_t i = 0; j >= 0 && i < POLLS / 16 &&
+                                 !bar_poll(empty(j % T::STAGES), (j / T::STAGES) & 1); ++i)
+                ;
+        }
     } else if (warp >= 2) {
         const int quarter = warp & 3;  // TMEM lanes 32 quarter .. + 31
         int tile = 0;
