@@ -115,7 +115,9 @@ __device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
-// False when the wait ran out or another role of the CTA has given up.
+// False when the wait ran out or another role of the CTA has given up. Lanes may see the
+// two in another order: no warp barrier lies inside a loop that a lane leaves over this, and the
+// lanes of a role agree once a tile. (A vote after each wait cost the large product 377 -> 405 us.)
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag)
 {
     for (uint32_t i = 0; i < POLLS; ++i) {
@@ -385,6 +387,7 @@ __global__ void __launch_bounds__(GTHREADS, 1)
 
     if (warp == 0) {
         const bool leader = elect_one();
+        const int lead = __ffs(__ballot_sync(0xFFFFFFFFu, leader)) - 1;
         int it = 0;
         bool ok = true;
         for (int64_t item = first_item; ok && item < walk.total; item += step) {
@@ -427,13 +430,14 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                         bulk_load(sc + T::SW, as + (int64_t)c * APC * ATOM, n, full(s));
                     }
                 }
-                __syncwarp();
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
+        it = __shfl_sync(0xFFFFFFFFu, it, lead);  // stages issued
         // The releases of the last stages are arrivals of commits that nothing above waits for,
         // a pair's in both CTAs: they land before the memory of their barriers is given back.
         for (int j = it < T::STAGES ? 0 : it - T::STAGES; ok && j < it; ++j)
-            ok = bar_wait(empty(j % T::STAGES), (j / T::STAGES) & 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, bar_wait(empty(j % T::STAGES), (j / T::STAGES) & 1, abort_flag));
         if (!ok) {
             if (lane == 0)
                 atomicAdd(p.err, 1u);
@@ -445,6 +449,7 @@ __global__ void __launch_bounds__(GTHREADS, 1)
         }
     } else if (warp == 1 && rank == 0) {
         const bool leader = elect_one();
+        const int lead = __ffs(__ballot_sync(0xFFFFFFFFu, leader)) - 1;
         int it = 0, tile = 0;
         bool ok = true;
         for (int64_t item = first_item; ok && item < walk.total; item += step, ++tile) {
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(GTHREADS, 1)
             if (T::SHARE > 0 ? tile >= 1 : tile >= 2) {
                 const int b = T::SHARE > 0 ? buf ^ 1 : buf;
                 const int phase = T::SHARE > 0 ? (tile - 1) / 2 : (tile - 2) / 2;
-                if (!bar_wait(acc_free(b), phase & 1, abort_flag)) {
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(acc_free(b), phase & 1, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -502,16 +507,16 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                     }
                     commit<PAIR>(empty(s));
                 }
-                __syncwarp();
             }
             if (ok && leader)
                 commit<PAIR>(acc_full(buf));
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
         if (!ok) {
             if (lane == 0)
                 atomicAdd(p.err, 1u);
             // products in flight end before their memory is given back
-            const int j = it - 1;
+            const int j = __shfl_sync(0xFFFFFFFFu, it, lead) - 1;
             for (uint32_t i = 0; j >= 0 && i < POLLS / 16 &&
                                  !bar_poll(empty(j % T::STAGES), (j / T::STAGES) & 1); ++i)
                 ;
