@@ -19,8 +19,8 @@
  * the kernels do with bad ones is said at each entry point.
  *
  * State beyond fp4q.h's list: the resident CTAs per SM of each row quantize
- * kernel, and one bit per product kernel and device (its shared-memory limit
- * has been raised). The product's waits are bounded like the TMA-fed
+ * kernel, and one bit per product or sort kernel and device (its shared-memory limit
+ * has been raised, to the most that any call needs). The product's waits are bounded like the TMA-fed
  * quantizer's; one that runs out ends the call early and adds to the counter of
  * fp4q_device_errors.
  *

@@ -178,6 +178,12 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
     }
 }
 
+// Dynamic shared memory of the placing kernel.
+size_t place_smem(int warps, int experts)
+{
+    return ((size_t)warps + 3) * experts * sizeof(int32_t);
+}
+
 template <class Id>
 cudaError_t sort_impl(const SortArgs& a, cudaStream_t st)
 {
@@ -200,13 +206,16 @@ cudaError_t sort_impl(const SortArgs& a, cudaStream_t st)
         if (e != cudaSuccess)
             return e;
     }
-    const size_t smem = ((size_t)(threads / 32) + 3) * a.experts * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(sort_place_kernel<Id>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const size_t smem = place_smem(threads / 32, a.experts);
+    // The limit belongs to the kernel, not to a call: the most that any call needs, once per
+    // device, so that no call depends on the sizes of others (before this one, or on other threads).
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = allow_smem(sort_place_kernel<Id>, place_smem(MAXW, FP4Q_MAX_EXPERTS), dev, done);
+    if (e != cudaSuccess)
+        return e;
     return launch_pdl(sort_place_kernel<Id>, dim3((unsigned)blocks), dim3(threads), smem, st, b);
 }
 
