@@ -145,7 +145,8 @@ fp4q_status fp4q_expert_gemm(const uint8_t* a_codes, const uint8_t* a_mma_scales
  *              everything behind it is a function of the input bits.
  * slots, n     int32 [n]: the rows to take (a value outside 0 .. rows-1 is skipped;
  *              a row named twice is written twice with the same bits), or
- *              NULL for all rows (n is ignored).
+ *              NULL for all rows (n is ignored; a call that takes none has rows 0 or
+ *              slots that are not NULL, n 0).
  * cols         a multiple of 32 and of rot (rows taken * cols / 32 at most
  *              0xF0000000); other arguments as fp4q_expert_quantize. global_amax_in NULL (NVFP4) takes the
  *              abs-max of the rotated h over the rows taken, and s_g from it as there. Without slots,

@@ -140,6 +140,19 @@ def _plan_args(plan: ExpertPlan, device) -> None:
         raise ValueError(f"plan.rows must be a multiple of {SEGMENT_ROWS}, got {plan.rows}")
 
 
+def _rows_taken(plan: Optional[ExpertPlan], rows: int, device):
+    """(rows, slots, their number) of a call over a plan's rows of a [rows, ...] input, over all without one.
+    To the library no slots means all rows, and an empty tensor's address is none: a plan without a choice
+    takes no row, so its call has none."""
+    if plan is None:
+        return rows, None, rows
+    _plan_args(plan, device)
+    if plan.rows != rows:
+        raise ValueError(f"gu has {rows} rows, the plan {plan.rows}")
+    n = plan.slots.numel()
+    return (rows, plan.slots.data_ptr(), n) if n else (0, None, 0)
+
+
 @functools.lru_cache(maxsize=4096)
 def scale_bytes(rows: int, cols: int, fmt="nvfp4") -> int:
     """Bytes of the MMA-layout scales of [rows, cols] (0 rows or columns: 0)."""
@@ -312,16 +325,11 @@ def glu_quantize(gu: torch.Tensor, fmt="nvfp4", strategy="absmax", rot: int = 0,
     cols, odd = cols // 2, cols % 2
     if odd:
         raise ValueError("gu must have an even number of columns")
-    if plan is not None:
-        _plan_args(plan, dev)
-        if plan.rows != rows:
-            raise ValueError(f"gu has {rows} rows, the plan {plan.rows}")
+    taken, slots, n = _rows_taken(plan, rows, dev)
     f = _fmt(fmt)
     out = _quantized_out(out, rows, cols, f, dq_dtype, dev)
     amax, work = _amax_args(f, global_amax, dev)
-    _call("fp4q_glu_quantize", dev, gu.data_ptr(), rows, cols,
-          plan.slots.data_ptr() if plan is not None else None,
-          plan.slots.numel() if plan is not None else rows, _act(act), f, _strategy(strategy), rot,
+    _call("fp4q_glu_quantize", dev, gu.data_ptr(), taken, cols, slots, n, _act(act), f, _strategy(strategy), rot,
           _ptr(amax), _ptr(out.global_scale) if f == 0 else None, _ptr(work), out.codes.data_ptr(),
           out.scales.data_ptr(), _ptr(out.dq), _DTYPES[out.dq.dtype] if out.dq is not None else 0)
     return out
@@ -337,17 +345,13 @@ def glu_bwd(gu: torch.Tensor, dh: torch.Tensor, plan: Optional[ExpertPlan] = Non
     _need(dh, "dh", dev, torch.bfloat16, rows, cols)
     if odd:
         raise ValueError("gu must have an even number of columns")
-    if plan is not None:
-        _plan_args(plan, dev)
-        if plan.rows != rows:
-            raise ValueError(f"gu has {rows} rows, the plan {plan.rows}")
+    taken, slots, n = _rows_taken(plan, rows, dev)
     if out is None:
         out = torch.empty_like(gu)
     else:
         _need(out, "out", dev, torch.bfloat16, rows, 2 * cols)
-    _call("fp4q_glu_bwd", dev, gu.data_ptr(), dh.data_ptr(), rows, cols,
-          plan.slots.data_ptr() if plan is not None else None,
-          plan.slots.numel() if plan is not None else rows, _act(act), rot, out.data_ptr())
+    _call("fp4q_glu_bwd", dev, gu.data_ptr(), dh.data_ptr(), taken, cols, slots, n, _act(act), rot,
+          out.data_ptr())
     return out
 
 

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import expert_ref as ref
+from microscaling_fp4_quantization_bf16_b200.experts import scale_bytes
 from test_gpu_experts import check_product, filled, operands, untouched
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +100,38 @@ def test_sorts_of_two_threads(gpu):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+# ---------------------------------------------------------------- a plan without tokens
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("calibrated", [False, True])
+def test_plan_without_tokens_takes_no_row(gpu, fmt, calibrated):
+    """A batch without a token in buffers of a fixed size: no row holds a choice, so none is read or written."""
+    rows, cols = 256, 64
+    p = gpu.expert_sort(torch.empty(0, 2, dtype=torch.int64, device="cuda"), 4, rows=rows)
+    assert p.rows == rows and p.starts.tolist() == [0] * 5
+    gu = torch.full((rows, 2 * cols), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q = gpu.Quantized(filled((rows, cols // 2), torch.uint8), filled((scale_bytes(rows, cols, fmt),), torch.uint8),
+                      torch.zeros(1, device="cuda") if fmt == "nvfp4" else None, None, filled((rows, cols), torch.float32))
+    amax = torch.full((1,), 5.0, device="cuda") if calibrated else None
+    gpu.glu_quantize(gu, fmt, plan=p, global_amax=amax, out=q)
+    assert untouched(q.codes, []) and untouched(q.dq, []) and untouched(q.scales[:, None], [])
+    assert fmt == "mxfp4" or q.global_scale.item() == 1.0
+    out = filled((rows, 2 * cols), torch.bfloat16)
+    gpu.glu_bwd(gu, torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda"), p, out=out)
+    assert untouched(out, [])
+    # and without a plan all rows are taken, as before
+    ones = torch.ones(3, 2 * cols, dtype=torch.bfloat16, device="cuda")
+    assert (gpu.glu_quantize(ones, fmt, dq_dtype=torch.float32).dq != 0).all()
+    # the layer's other calls on such a plan
+    x = torch.empty(0, cols, dtype=torch.bfloat16, device="cuda")
+    gpu.expert_quantize(x, p, fmt, global_amax=amax, out=q)
+    assert untouched(q.codes, []) and untouched(q.dq, []) and untouched(q.scales[:, None], [])
+    w = gpu.expert_weights(torch.ones(4, 16, cols, dtype=torch.bfloat16, device="cuda"), fmt)
+    d = filled((rows, 16), torch.bfloat16)
+    gpu.expert_gemm(q.codes, q.scales, q.global_scale, w.codes, w.scales, w.global_scale, p, fmt, out=d)
+    assert untouched(d, [])
+    assert gpu.expert_combine(d, p).shape == (0, 16)
+    dy, dw = gpu.expert_combine_bwd(torch.empty(0, 16, dtype=torch.bfloat16, device="cuda"), d, p, out=filled((rows, 16), torch.bfloat16))
+    assert untouched(dy, []) and dw.shape == (0, 2)
