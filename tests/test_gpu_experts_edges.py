@@ -11,7 +11,7 @@ import torch
 
 import expert_ref as ref
 from microscaling_fp4_quantization_bf16_b200.experts import scale_bytes
-from test_gpu_experts import check_product, filled, operands, untouched
+from test_gpu_experts import U24, UBF, check_product, filled, operands, untouched
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,32 @@ def test_plan_without_tokens_takes_no_row(gpu, fmt, calibrated):
     assert gpu.expert_combine(d, p).shape == (0, 16)
     dy, dw = gpu.expert_combine_bwd(torch.empty(0, 16, dtype=torch.bfloat16, device="cuda"), d, p, out=filled((rows, 16), torch.bfloat16))
     assert untouched(dy, []) and dw.shape == (0, 2)
+
+
+# ---------------------------------------------------------------- gradients at the ends of the types' range
+
+def glu_gradient_bound(g, u, d, act):
+    """64-bit gradient [dg, du] and the bound of glu_bwd's fp32 steps: s off by 2^-20 + 2^-21 max(-z, 0) relative (hardware
+    2^x and 1/x), every other step by a few half steps; the two terms of a'(g) may cancel, so their magnitudes
+    count; one bf16 rounding; s below 2^-126 counts as zero."""
+    z, dz = ref.gate(g, act)
+    s = ref.sigmoid(z)
+    want = np.concatenate([d * u * (s + g * s * (1 - s) * dz), d * g * s], 1)
+    es = np.where(s < 2.0 ** -125, 1.0, (2.0 ** -20 + 2.0 ** -21 * np.maximum(-z, 0)) + 12 * U24)
+    size = np.concatenate([np.abs(d * u) * (s + np.abs(g) * s * (1 - s) * dz) * 3, np.abs(d * g) * s], 1)
+    bound = size * np.concatenate([es, es], 1)
+    return want, (bound + UBF * (np.abs(want) + bound)) * 1.01 + 2.0 ** -120
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_glu_gradient_of_far_gates(gpu, act):
+    """Gates up to the type's largest: a'(g) is 1 or 0 there, and never a number that is none."""
+    g = np.array([1e13, 1e15, 2.0 ** 63, 2.0 ** 64, 1e20, 1e30, 3e38, 3.3895313892515355e38])
+    g = np.concatenate([g, -g])[None]
+    u = np.tile([0.5, -0.75, 1.0, 2.0 ** -20], 4)[None]
+    dh = torch.from_numpy(np.tile([0.5, 0.25, -0.5, 1e-10], 4)[None]).to(torch.bfloat16)
+    gu = torch.from_numpy(np.concatenate([g, u], 1)).to(torch.bfloat16)
+    got = ref.to64(gpu.glu_bwd(gu.cuda(), dh.cuda(), None, act))
+    g, u = np.split(ref.to64(gu), 2, axis=1)
+    want, bound = glu_gradient_bound(g, u, ref.to64(dh), act)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all(), got
