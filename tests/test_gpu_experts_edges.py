@@ -164,3 +164,19 @@ def test_glu_gradient_of_far_gates(gpu, act):
     g, u = np.split(ref.to64(gu), 2, axis=1)
     want, bound = glu_gradient_bound(g, u, ref.to64(dh), act)
     assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all(), got
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_glu_gradient_whose_first_product_overflows(gpu, act):
+    """dh u beyond fp32 in front of a small a'(g): the gradient itself is in range."""
+    g = np.array([-80.0, -70.0, -60.0, -45.0, -200.0, -3e38, 0.0, -1.0]) if act == "silu" else \
+        np.array([-8.5, -8.0, -7.5, -6.5, -20.0, -3e38, 0.0, -1.0])
+    d = np.array([1e30, 1e25, -1e24, 1e19, 1e30, 1e30, 1e10, 1e10])
+    u = np.array([1e30, -1e30, 1e20, 1e30, 1e30, 1e30, 1e20, 1e20])
+    gu = torch.from_numpy(np.concatenate([g, u])[None]).to(torch.bfloat16)
+    dh = torch.from_numpy(d[None]).to(torch.bfloat16)
+    got = ref.to64(gpu.glu_bwd(gu.cuda(), dh.cuda(), None, act))
+    g, u = np.split(ref.to64(gu), 2, axis=1)
+    want, bound = glu_gradient_bound(g, u, ref.to64(dh), act)
+    assert (np.abs(ref.to64(dh) * u)[0, :6] > 3.4e38).all() and np.isfinite(want).all()
+    assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all(), (got, want)
