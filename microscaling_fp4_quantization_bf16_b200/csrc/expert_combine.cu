@@ -151,11 +151,13 @@ __global__ void __launch_bounds__(CTHREADS) combine_kernel(CombineArgs a)
 // One block: one token. Each thread walks the token's columns 8 at a time:
 // one read of g, one of each choice's row, one write of each choice's
 // gradient; the products with y stay in one 64-bit accumulator per choice (a
-// router's gradient is one number out of thousands of terms that may cancel; it costs 1 us of 47). Four choices
-// at a time: more of them in flight cost registers and thereby warps (4000 tokens x 4096 to four
-// experts: 52 us; 8 choices 67, two pieces of columns as well 61, both 104).
+// router's gradient is one number out of thousands of terms that may cancel), taken in 64 bits too: bf16
+// has fp32's exponents, so a product of two may be out of its range (4000 tokens x 4096 to four experts:
+// 48.7 us; with the products of two bf16 numbers in fp32 46.9). Four choices at a time: more of them
+// in flight cost registers and thereby warps (8 choices 67, two pieces of columns as well 61, both 104);
+// of bf16 arrays 7 CTAs an SM (without the bound 49.2).
 template <bool G32, bool Y32>
-__global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
+__global__ void __launch_bounds__(CTHREADS, G32 || Y32 ? 0 : 7) combine_bwd_kernel(CombineBwdArgs a)
 {
     constexpr int GROUP = 4;
     pdl_begin();
@@ -194,10 +196,7 @@ __global__ void __launch_bounds__(CTHREADS) combine_bwd_kernel(CombineBwdArgs a)
                         widen8<Y32>(p[j], v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if constexpr (G32 || Y32)
-                                acc[j] = __fma_rn((double)g[e], (double)v[e], acc[j]);
-                            else  // the product of two bf16 numbers is exact in fp32
-                                acc[j] = __dadd_rn(acc[j], (double)__fmul_rn(g[e], v[e]));
+                            acc[j] = __fma_rn((double)g[e], (double)v[e], acc[j]);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)

@@ -180,3 +180,40 @@ def test_glu_gradient_whose_first_product_overflows(gpu, act):
     want, bound = glu_gradient_bound(g, u, ref.to64(dh), act)
     assert (np.abs(ref.to64(dh) * u)[0, :6] > 3.4e38).all() and np.isfinite(want).all()
     assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all(), (got, want)
+
+
+@pytest.mark.parametrize("g32,y32", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("what", ["large", "small", "mixed"])
+def test_combine_gradient_beyond_the_products_range(gpu, g32, y32, what):
+    """Products of two bf16 numbers that fp32 does not hold, in sums that it does: dweights is summed in 64 bits."""
+    cols = 4096
+    p = gpu.expert_sort(torch.zeros(1, 1, dtype=torch.int64, device="cuda"), 1)
+    g, y = np.ones(cols), np.zeros((p.rows, cols))
+    if what == "large":                               # 2^128 and its opposite, and 3 beside them
+        g[:4], y[0, :4] = 2.0 ** 64, [2.0 ** 64, -2.0 ** 64, 2.0 ** 80, -2.0 ** 80]
+        y[0, 9] = 3.0
+        want = 3.0
+    elif what == "small":                             # 4096 times 2^-160
+        g[:], y[0] = 2.0 ** -80, 2.0 ** -80
+        want = 2.0 ** -148
+    else:                                             # subnormal products: 2^-140 (1 + 2^-7)^2 each, in 8 of which bits are lost
+        g[:], y[0] = 2.0 ** -70 * (1 + 2.0 ** -7), 2.0 ** -70 * (1 + 2.0 ** -7)
+        want = cols * 2.0 ** -140 * (1 + 2.0 ** -7) ** 2
+    g = torch.from_numpy(g[None]).to(torch.float32 if g32 else torch.bfloat16).cuda()
+    y = torch.from_numpy(y).to(torch.float32 if y32 else torch.bfloat16).cuda()
+    _, dw = gpu.expert_combine_bwd(g, y, p)
+    # every sum of these is exact in 64 bits; one rounding to fp32 (2^-148 is a subnormal that fp32 has)
+    assert abs(dw.item() - want) <= max(U24 * want, 2.0 ** -150), (dw.item(), want)
+
+
+def test_combine_gradient_of_infinities(gpu):
+    """An infinity or NaN in a row of y comes out in its own choice's gradient and in no other."""
+    cols = 512
+    p = gpu.expert_sort(torch.tensor([[0, 1, 2, 3]], device="cuda"), 4)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.ones(p.rows, cols, dtype=dtype, device="cuda")
+        r = p.slots[0].tolist()
+        y[r[0], 3], y[r[1], 300], y[r[2], 511] = float("inf"), float("-inf"), float("nan")
+        dy, dw = gpu.expert_combine_bwd(torch.ones(1, cols, dtype=dtype, device="cuda"), y, p)
+        assert dw[0, 0] == float("inf") and dw[0, 1] == float("-inf") and dw[0, 2].isnan() and dw[0, 3] == cols
+        assert (dy[p.slots[0].long()] == 1).all()
