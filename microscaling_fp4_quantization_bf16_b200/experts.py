@@ -88,6 +88,13 @@ def _matrix(t, name: str, device, dtype):
     return shape
 
 
+def _result(dtype, name: str):
+    """dtype, if results can have it."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+    return dtype
+
+
 def _fmt(fmt) -> int:
     f = _FORMATS.get(fmt) if isinstance(fmt, str) else fmt
     if f not in (0, 1):
@@ -210,7 +217,7 @@ def _quantized_out(out, rows: int, cols: int, f: int, dq_dtype, device):
             return torch.empty(shape, dtype=dtype, device=device)
         return Quantized(new((rows, cols // 2), torch.uint8), new((size,), torch.uint8),
                          new((1,), torch.float32) if f == 0 else None, None,
-                         new((rows, cols), dq_dtype) if dq_dtype is not None else None)
+                         new((rows, cols), _result(dq_dtype, "dq_dtype")) if dq_dtype is not None else None)
     _need(out.codes, "out.codes", device, torch.uint8, rows, cols // 2)
     _need(out.scales, "out.scales", device, torch.uint8, size)
     if f == 0:
@@ -285,7 +292,7 @@ def expert_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scale: O
     f = _fmt(fmt)
     dev = _device(w_codes, "w_codes")
     _need(w_codes, "w_codes", dev, torch.uint8)
-    if w_codes.dim() != 3:
+    if w_codes.dim() != 3 or w_codes.shape[0] == 0:
         raise ValueError(f"w_codes must have shape [experts, N, K/2], got {tuple(w_codes.shape)}")
     experts, n, half = w_codes.shape
     k = 2 * half
@@ -302,7 +309,7 @@ def expert_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scale: O
     else:
         a_global_scale = w_global_scale = None
     if out is None:
-        out = torch.empty(rows, n, dtype=out_dtype, device=dev)
+        out = torch.empty(rows, n, dtype=_result(out_dtype, "out_dtype"), device=dev)
     else:
         _need(out, "out", dev, (torch.float32, torch.bfloat16), rows, n)
     choices = plan.slots.numel()
@@ -370,7 +377,7 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
     if weights is not None:
         _need(weights, "weights", dev, torch.float32, tokens, k)
     if out is None:
-        out = torch.empty(tokens, cols, dtype=out_dtype, device=dev)
+        out = torch.empty(tokens, cols, dtype=_result(out_dtype, "out_dtype"), device=dev)
     else:
         _need(out, "out", dev, (torch.float32, torch.bfloat16), tokens, cols)
     _call("fp4q_expert_combine", dev, y.data_ptr(), _DTYPES[y.dtype], plan.rows, cols,

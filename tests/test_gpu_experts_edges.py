@@ -217,3 +217,22 @@ def test_combine_gradient_of_infinities(gpu):
         dy, dw = gpu.expert_combine_bwd(torch.ones(1, cols, dtype=dtype, device="cuda"), y, p)
         assert dw[0, 0] == float("inf") and dw[0, 1] == float("-inf") and dw[0, 2].isnan() and dw[0, 3] == cols
         assert (dy[p.slots[0].long()] == 1).all()
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_refused_output_types_and_no_experts(gpu):
+    """Types that no output has and weights of no expert raise as the other arguments do, before anything runs."""
+    p = gpu.expert_sort(torch.zeros(4, 2, dtype=torch.int64, device="cuda"), 4)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(p.rows, 64, dtype=torch.bfloat16, device="cuda")
+    q = gpu.expert_quantize(x, p, "mxfp4")
+    w = gpu.expert_weights(torch.zeros(4, 32, 64, dtype=torch.bfloat16, device="cuda"), "mxfp4")
+    none = gpu.ExpertPlan(p.counts[:0], p.starts[:1], p.slots, p.rows)
+    for call in (lambda: gpu.expert_quantize(x, p, "mxfp4", dq_dtype=torch.float16),
+                 lambda: gpu.glu_quantize(x, "mxfp4", dq_dtype=torch.float64),
+                 lambda: gpu.expert_combine(y, p, out_dtype=torch.float16),
+                 lambda: gpu.expert_gemm(q.codes, q.scales, None, w.codes, w.scales, None, p, "mxfp4", torch.float16),
+                 lambda: gpu.expert_gemm(q.codes, q.scales, None, w.codes[:0], w.scales[:0], None, none, "mxfp4")):
+        with pytest.raises(ValueError):
+            call()
