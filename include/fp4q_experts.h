@@ -92,7 +92,7 @@ fp4q_status fp4q_expert_sort(const void* ids, int id_bytes, int64_t n, int64_t e
  *              2688, one division, as fp4q_quantize), or NULL to
  *              take the abs-max of all of x (rotated; tokens without a choice
  *              included) in an extra pass; s_g is then that maximum times fp32(1 / 2688), which
- *              may be one unit in the last place from the quotient (for
+ *              may be one unit in the last place from the quotient, and codes at ties with it (for
  *              fp4q_quantize's own bits pass fp4q_global_amax's value). Ignored for MXFP4.
  * global_scale_out NVFP4: device float, receives s_g.
  * amax_work    FP4Q_AMAX_WORK device floats of scratch, needed when fmt is NVFP4 and
@@ -165,7 +165,7 @@ fp4q_status fp4q_glu_quantize(const void* gu, int64_t rows, int64_t cols, const 
  * quantizer: dh is first taken back through the rotation (dh <- R dh, blockwise;
  * R is its own transpose), then du = dh a(g), dg = dh u a'(g),
  * a'(g) = s + g s (1 - s) z'(g), s = sigmoid(z(g)). fp32 throughout, rounded
- * once to bf16.
+ * once to bf16. s below 2^-126 counts as zero.
  * gu           bf16 [rows, 2 * cols]; dh bf16 [rows, cols]; cols a multiple of
  *              8 and of rot (of 32 for rot > 0).
  * slots, n     as fp4q_glu_quantize.

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(CTHREADS, G32 || Y32 ? 0 : 7) combine_bwd_kern
     }
 }
 
-// sigmoid(z) in fp32: a few units in the last place; 0 for z below -88.
+// sigmoid(z) in fp32: a few units in the last place; 0 where it is below 2^-126 (z below -87.3).
 __device__ __forceinline__ float sigmoid(float z)
 {
     return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-z)));

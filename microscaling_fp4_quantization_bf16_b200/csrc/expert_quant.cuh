@@ -3,7 +3,9 @@
 //
 // Arithmetic: process_segment of quant_kernel.cuh, one thread to a 32-element
 // segment, so codes, scales and values are bit for bit those of the plain
-// quantizer. A token is read and quantized once however many experts take it.
+// quantizer under the same s_g. That is the same number for a given abs-max; without one it may be a
+// unit in the last place apart (see row_scale_tables). A token is read and quantized once however
+// many experts take it.
 //
 // Memory: each warp brings its next 32 segments (2 KB of bf16, twice that for
 // gate and value) into shared memory with 16-byte asynchronous copies while it
@@ -21,7 +23,7 @@
 // Bound by: with values written, tokens by memory (16384 x 8192 to two experts
 // each, 4-over-6: 936 MB in 184 us, 5.1 TB/s, seven tenths writes); without,
 // by instruction issue (133 us for one expert each); behind the activation by
-// instruction issue (7946 x 14336, MXFP4 H128, values: 744 MB in 168 us, about 34
+// instruction issue (7946 x 14336, MXFP4 H128, values: 744 MB in 168 us, about 33
 // instructions a value at 0.66 per scheduler and clock).
 #pragma once
 
@@ -232,8 +234,9 @@ __device__ __forceinline__ void store_rows(const RowQuantArgs& a, const Segment&
 // The NVFP4 tables of a CTA (see ScaleTables), from the calibrated abs-max, or
 // from the maxima of the abs-max pass's CTAs: every CTA joins them itself
 // (no launch in between, no value to clear beforehand), and takes s_g as their maximum times
-// 1 / 2688, one product, where a calibrated abs-max is divided. CTA 0 publishes s_g. Ends
-// with a CTA barrier.
+// fp32(1 / 2688), one product, where a calibrated abs-max is divided: what the header says of each. The
+// product is a unit from the quotient for 22 maxima in a hundred (off by 0.81 of a unit at most,
+// the quotient by 0.5), and codes that lie on a tie go with it. CTA 0 publishes s_g. Ends with a CTA barrier.
 template <int STRAT>
 __device__ __forceinline__ void row_scale_tables(const RowQuantArgs& a, ScaleTables<STRAT>& tab)
 {

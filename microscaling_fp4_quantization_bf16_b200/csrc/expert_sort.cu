@@ -13,8 +13,8 @@
 // Up to SUB choices one block does it all in one launch: what counts is
 // the launch and a dozen barriers, not bandwidth. Above, a first kernel counts the ids of each
 // block's chunk (one block per SM at most), and the second adds up the counts of the blocks
-// before it; it reads the ids a second time, from L2. (64 x 2 choices of 8 experts: 6 us with
-// the launch; 65536 x 8 of 256: 19 us, of which reading 4 MB would take 1.)
+// before it; it reads the ids a second time, from L2. (64 x 2 choices of 8 experts: a kernel of 5 us;
+// 65536 x 8 of 256: 4 and 15 us, 19.5 cold with the launches, of which reading 4 MB would take 1.)
 #include "experts.h"
 #include "fp4q_device.cuh"
 
