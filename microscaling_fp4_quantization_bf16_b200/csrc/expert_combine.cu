@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(CTHREADS) combine_kernel(CombineArgs a)
 // gradient; the products with y stay in one 64-bit accumulator per choice (a
 // router's gradient is one number out of thousands of terms that may cancel), taken in 64 bits too: bf16
 // has fp32's exponents, so a product of two may be out of its range (4000 tokens x 4096 to four experts:
-// 48.7 us; with the products of two bf16 numbers in fp32 46.9). Four choices at a time: more of them
-// in flight cost registers and thereby warps (8 choices 67, two pieces of columns as well 61, both 104);
-// of bf16 arrays 7 CTAs an SM (without the bound 49.2).
+// 48.7 us back to back; with the products of two bf16 numbers in fp32 46.9). Four choices at a time: more
+// of them in flight cost registers and thereby warps (cold, with fp32 products: 52 us; 8 choices 67,
+// two pieces of columns as well 61, both 104); of bf16 arrays 7 CTAs an SM (without the bound 49.2).
 template <bool G32, bool Y32>
 __global__ void __launch_bounds__(CTHREADS, G32 || Y32 ? 0 : 7) combine_bwd_kernel(CombineBwdArgs a)
 {
